@@ -114,7 +114,7 @@ def _quantize_plain(v, rows, scale):
     t = _padded(v, rows)
     a = t.abs().amax((1, 3))
     if scale == "f32":
-        s = (a / _E4M3_MAX).clamp_min(2.0 ** -126)
+        s = (a / torch.full_like(a, _E4M3_MAX)).clamp_min(2.0 ** -126)   # a quotient: a number would be inverted first
         s = torch.where(torch.isfinite(a), s, torch.nan)
         out = s
     else:
