@@ -75,7 +75,7 @@ typedef enum {
   FP4Q_OK = 0,
   FP4Q_ERR_ARG = 1,          /* null pointer where one is required, bad plan handle  */
   FP4Q_ERR_SHAPE = 2,        /* M, K outside the shape rules                          */
-  FP4Q_ERR_ALIGN = 3,        /* a pointer is not 16-byte aligned                      */
+  FP4Q_ERR_ALIGN = 3,        /* a pointer is not aligned as its call asks             */
   FP4Q_ERR_UNSUPPORTED = 4,  /* format / group / block / rule combination not offered */
   FP4Q_ERR_CUDA = 5,         /* a CUDA runtime call failed                            */
   FP4Q_ERR_TIMEOUT = 6       /* a bounded wait inside a kernel ran out                */
@@ -242,6 +242,67 @@ fp4q_status fp4q_dequantize_mbs(fp4q_plan plan, const void* codes, const void* s
 fp4q_status fp4q_gemm(int format, const void* a_codes, const void* a_scales, const float* a_tensor_scale,
                       const void* b_codes, const void* b_scales, const float* b_tensor_scale, int64_t M,
                       int64_t N, int64_t K, void* d_bf16, void* stream);
+
+/* ---- 8-bit linear layers: E4M3 codes with a scale per 128 channels.
+ *
+ * For the layers that a deployment keeps out of FP4: the RMS norm in front of a projection, the
+ * quantizer for the activations that no norm precedes and for the weights, and the product of the
+ * two.  The pages have no counterpart; codes, scales and layouts follow the rest of this header.
+ *
+ * Layout: codes uint8 [rows][K] (E4M3), row-major and contiguous; scales row-major and contiguous,
+ * [rows][ceil(K / 128)] for activations (a scale per row and 128 channels), [ceil(rows / 128)]
+ * [ceil(K / 128)] for weights (a scale per 128 x 128 tile).  K is a multiple of 16; the last block
+ * of a row and the last tile of the weights may be short.
+ *
+ * Rules, with y the fp32 values of a block and A their largest magnitude:
+ *   FP4Q_FP8_SCALE_F32   fp32 scale s = max(RN(A / 448), 2^-126);
+ *   FP4Q_FP8_SCALE_E8M0  s = 2^e held as the byte e + 127, e the least integer with 448 * 2^e >= A,
+ *                        and at least -126;
+ *   code = E4M3(y / s), the quotient rounded to fp32 (correctly while s >= 2^-90; one ulp below) and
+ *   then to nearest even, saturating at 448.
+ * A block of zeros so has the scale 2^-126.  A block that holds a NaN or an infinity has the scale
+ * NaN (E8M0: byte 255) and NaN codes throughout.
+ *
+ * These calls own nothing and allocate nothing; calls on different streams are independent.  Every
+ * array belongs to the CUDA context that is current, as the stream does.  An output that overlaps
+ * an input or another output is refused with FP4Q_ERR_ARG, but for the two cases fp4q_add_rmsnorm_fp8
+ * names. */
+typedef enum { FP4Q_FP8_SCALE_F32 = 0, FP4Q_FP8_SCALE_E8M0 = 1 } fp4q_fp8_scale;
+typedef enum { FP4Q_DTYPE_BF16 = 0, FP4Q_DTYPE_FP16 = 1, FP4Q_DTYPE_F32 = 2 } fp4q_dtype;
+
+/* Quantize X [M][K] (dtype FP4Q_DTYPE_BF16 or _FP16; rows ldx elements apart, ldx >= K and a multiple
+ * of 8; 16-byte aligned) to codes and scales.  block_rows: 1 (activations) or 128 (weights).
+ * codes_out 16-byte aligned; scales_out 4-byte aligned (F32) or any (E8M0).  M >= 0,
+ * M * ceil(K / 128) < 2^31, M * ldx <= 2^40; an empty X launches nothing.  Bit-exact by the rules above. */
+fp4q_status fp4q_quantize_fp8(int scale_format, int dtype, int block_rows, const void* x, int64_t ldx, int64_t M,
+                              int64_t K, void* codes_out, void* scales_out, void* stream);
+
+/* Residual addition, RMS norm and 8-bit quantization of rows of activations in one pass:
+ *   h = x + residual (x alone when residual is NULL), in fp32;  residual_out = h rounded to dtype;
+ *   y = h / sqrt(mean(h^2) + eps) * weight, in fp32, of h as it was before that rounding;
+ *   codes and scales of y per row and 128 channels, by the rules above.
+ * x, residual, residual_out: dtype [M][K], rows ldx, ldr, ldo elements apart (each >= K and a multiple
+ * of 8), 16-byte aligned; weight: dtype [K], 16-byte aligned.  residual and residual_out are both given
+ * or both NULL (ldr and ldo are then ignored).  residual_out may be residual itself (with ldo = ldr) or
+ * x itself (with ldo = ldx).  eps: finite, >= 0.  K at most 32768; the rest as for fp4q_quantize_fp8.
+ * The sum of squares is fp32, in a fixed order: the result of a row depends on that row and K alone.
+ * Rows whose sum of squares passes fp32's range give zeros, as 1 / sqrt(inf) does. */
+fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int64_t ldx, const void* residual,
+                                 int64_t ldr, const void* weight, float eps, int64_t M, int64_t K,
+                                 void* residual_out, int64_t ldo, void* codes_out, void* scales_out, void* stream);
+
+/* 8-bit GEMM on the tensor cores: D = A * B^T with
+ *   D[m][n] = sum_j a_scales[m][j] * b_scales[n / 128][j] * sum_{k in block j} a_codes[m][k] b_codes[n][k],
+ * A [M][K] an activation's codes and scales (block_rows 1, or fp4q_add_rmsnorm_fp8's), B [N][K] a
+ * weight's (block_rows 128), both of scale_format.  d: out_dtype (FP4Q_DTYPE_BF16, _FP16 or _F32) [M][N],
+ * row-major and contiguous, 16-byte aligned.  Sums are fp32: a block's on the tensor core
+ * (tcgen05 kind::f8f6f4), the blocks' in registers; D is rounded once.  Any scale bytes and codes are
+ * taken, NaN ones too.  M, N >= 0 and K a positive multiple of 16 (an empty M or N launches nothing),
+ * each below 2^31 - 512, their pairwise products at most 2^40.  Codes 16-byte aligned, scales as in
+ * fp4q_quantize_fp8.  Deterministic. */
+fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
+                          const void* b_codes, const void* b_scales, int64_t M, int64_t N, int64_t K, void* d,
+                          void* stream);
 
 /* No-allocation NVFP4 dynamic-scale path.  The paper has no counterpart: this exists for
  * callers that cannot allocate device memory themselves — for example a library loaded into

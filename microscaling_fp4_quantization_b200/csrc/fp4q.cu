@@ -94,7 +94,8 @@ fp4q_status bound_context_id(uint64_t* out) {
   return current_context_id(out);
 }
 
-fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes) {
+fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes,
+                             int carveout) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -114,8 +115,8 @@ fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, Ke
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, attr_smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-  // all of the unified L1 / shared storage as shared memory: these kernels stage through it
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+  // 100: all of the unified L1 / shared storage as shared memory, for the kernels that stage through it
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(carveout)");
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ki.ctas_per_sm, kernel, threads, smem_bytes);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
@@ -778,6 +779,105 @@ fp4q_status fp4q_gemm(int format, const void* a_codes, const void* a_scales, con
   return launch_gemm<kNV>(ac, as, a_tensor_scale, bc, bs, b_tensor_scale, M, N, K, d, s);
 }
 
+namespace {
+
+// The first and one-past-last byte of `rows` rows of K elements, ld elements apart.
+struct ByteRange {
+  uintptr_t lo, hi;
+  ByteRange(const void* p, int64_t rows, int64_t K, int64_t ld, int64_t esize)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + static_cast<uintptr_t>(((rows - 1) * ld + K) * esize) : lo) {}
+  bool overlaps(const ByteRange& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Shape rules of the 8-bit quantizing calls: rows of K 16-bit elements, ld apart.
+fp4q_status check_fp8_rows(int64_t M, int64_t K, int64_t ld) {
+  if (M < 0 || K < 0 || K % 16 != 0 || K > (int64_t(1) << 31) - 128) return FP4Q_ERR_SHAPE;
+  if (ld < K || ld % 8 != 0) return FP4Q_ERR_SHAPE;
+  if (K > 0 && M > ((int64_t(1) << 31) - 1) / ((K + 127) / 128)) return FP4Q_ERR_SHAPE;
+  if (M > 0 && ld > (int64_t(1) << 40) / M) return FP4Q_ERR_SHAPE;
+  return FP4Q_OK;
+}
+
+bool valid_fp8_scale(int f) { return f == FP4Q_FP8_SCALE_F32 || f == FP4Q_FP8_SCALE_E8M0; }
+uintptr_t fp8_scale_align(int f) { return f == FP4Q_FP8_SCALE_F32 ? 4 : 1; }
+int64_t fp8_scale_bytes(int f) { return f == FP4Q_FP8_SCALE_F32 ? 4 : 1; }
+
+}  // namespace
+
+fp4q_status fp4q_quantize_fp8(int scale_format, int dtype, int block_rows, const void* x, int64_t ldx, int64_t M,
+                              int64_t K, void* codes_out, void* scales_out, void* stream) {
+  if (!valid_fp8_scale(scale_format) || (dtype != FP4Q_DTYPE_BF16 && dtype != FP4Q_DTYPE_FP16) ||
+      (block_rows != 1 && block_rows != 128))
+    return FP4Q_ERR_UNSUPPORTED;
+  fp4q_status st = check_fp8_rows(M, K, ldx);
+  if (st != FP4Q_OK) return st;
+  if (M == 0 || K == 0) return FP4Q_OK;
+  if (!x || !codes_out || !scales_out) return FP4Q_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(codes_out, 16) || !aligned(scales_out, fp8_scale_align(scale_format)))
+    return FP4Q_ERR_ALIGN;
+  const int64_t kb = (K + 127) / 128, rb = (M + block_rows - 1) / block_rows;
+  const ByteRange rx(x, M, K, ldx, 2), rc(codes_out, M, K, K, 1),
+      rs(scales_out, rb, kb, kb, fp8_scale_bytes(scale_format));
+  if (rx.overlaps(rc) || rx.overlaps(rs) || rc.overlaps(rs)) return FP4Q_ERR_ARG;
+  return launch_quantize_fp8(scale_format, dtype, block_rows, x, ldx, M, K, codes_out, scales_out,
+                             static_cast<cudaStream_t>(stream));
+}
+
+fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int64_t ldx, const void* residual,
+                                 int64_t ldr, const void* weight, float eps, int64_t M, int64_t K,
+                                 void* residual_out, int64_t ldo, void* codes_out, void* scales_out, void* stream) {
+  if (!valid_fp8_scale(scale_format) || (dtype != FP4Q_DTYPE_BF16 && dtype != FP4Q_DTYPE_FP16))
+    return FP4Q_ERR_UNSUPPORTED;
+  if ((residual != nullptr) != (residual_out != nullptr)) return FP4Q_ERR_ARG;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return FP4Q_ERR_ARG;   // negative, NaN or infinite
+  fp4q_status st = check_fp8_rows(M, K, ldx);
+  if (st == FP4Q_OK && residual) st = check_fp8_rows(M, K, ldr);
+  if (st == FP4Q_OK && residual) st = check_fp8_rows(M, K, ldo);
+  if (st != FP4Q_OK) return st;
+  if (K > 32768) return FP4Q_ERR_SHAPE;   // a row is held in one CTA's registers
+  if (M == 0 || K == 0) return FP4Q_OK;
+  if (!x || !weight || !codes_out || !scales_out) return FP4Q_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(codes_out, 16) ||
+      !aligned(scales_out, fp8_scale_align(scale_format)) || !aligned(residual, 16) || !aligned(residual_out, 16))
+    return FP4Q_ERR_ALIGN;
+  const int64_t kb = (K + 127) / 128;
+  const ByteRange rx(x, M, K, ldx, 2), rr(residual, M, K, ldr, 2), rw(weight, 1, K, K, 2),
+      ro(residual_out, M, K, ldo, 2), rc(codes_out, M, K, K, 1), rs(scales_out, M, kb, kb, fp8_scale_bytes(scale_format));
+  for (const ByteRange* out : {&rc, &rs})
+    if (out->overlaps(rx) || out->overlaps(rr) || out->overlaps(rw) || out->overlaps(ro)) return FP4Q_ERR_ARG;
+  if (rc.overlaps(rs) || ro.overlaps(rw)) return FP4Q_ERR_ARG;
+  // the sum may be stored over x or over the residual (each element is read by the thread that
+  // writes it, before it does), but over neither shifted
+  if (ro.overlaps(rx) && (residual_out != x || ldo != ldx)) return FP4Q_ERR_ARG;
+  if (ro.overlaps(rr) && (residual_out != residual || ldo != ldr)) return FP4Q_ERR_ARG;
+  return launch_add_rmsnorm_fp8(scale_format, dtype, x, ldx, residual, ldr, weight, eps, M, K, residual_out, ldo,
+                                codes_out, scales_out, static_cast<cudaStream_t>(stream));
+}
+
+fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
+                          const void* b_codes, const void* b_scales, int64_t M, int64_t N, int64_t K, void* d,
+                          void* stream) {
+  if (!valid_fp8_scale(scale_format) ||
+      (out_dtype != FP4Q_DTYPE_BF16 && out_dtype != FP4Q_DTYPE_FP16 && out_dtype != FP4Q_DTYPE_F32))
+    return FP4Q_ERR_UNSUPPORTED;
+  constexpr int64_t kMaxDim = (int64_t(1) << 31) - 512;   // 32-bit TMA coordinates, with a tile past the end
+  if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP4Q_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP4Q_OK;
+  if (K == 0) return FP4Q_ERR_SHAPE;   // an empty reduction, as in fp4q_gemm
+  if (M > (int64_t(1) << 40) / K || N > (int64_t(1) << 40) / K || M > (int64_t(1) << 40) / N) return FP4Q_ERR_SHAPE;
+  if (!a_codes || !a_scales || !b_codes || !b_scales || !d) return FP4Q_ERR_ARG;
+  if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(d, 16) ||
+      !aligned(a_scales, fp8_scale_align(scale_format)) || !aligned(b_scales, fp8_scale_align(scale_format)))
+    return FP4Q_ERR_ALIGN;
+  const int64_t kb = (K + 127) / 128, sb = fp8_scale_bytes(scale_format);
+  const ByteRange rd(d, M, N, N, out_dtype == FP4Q_DTYPE_F32 ? 4 : 2);
+  if (rd.overlaps(ByteRange(a_codes, M, K, K, 1)) || rd.overlaps(ByteRange(b_codes, N, K, K, 1)) ||
+      rd.overlaps(ByteRange(a_scales, M, kb, kb, sb)) || rd.overlaps(ByteRange(b_scales, (N + 127) / 128, kb, kb, sb)))
+    return FP4Q_ERR_ARG;
+  return launch_gemm_fp8(scale_format, out_dtype, a_codes, a_scales, b_codes, b_scales, M, N, K, d,
+                         static_cast<cudaStream_t>(stream));
+}
+
 fp4q_status fp4q_selftest_wait_timeout(void* stream) {
   return launch_wait_timeout_selftest(static_cast<cudaStream_t>(stream));
 }
@@ -787,7 +887,7 @@ fp4q_status fp4q_device_status(void) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
   unsigned int v = 0;
   for (fp4q_status (*reader)(unsigned int*) : {status_rq_mx, status_rq_nv, status_mbs, status_qe, status_mma,
-                                               status_mma_qe, status_dequant, status_gemm}) {
+                                               status_mma_qe, status_dequant, status_gemm, status_gemm_fp8}) {
     fp4q_status st = reader(&v);
     if (st != FP4Q_OK) return st;
   }
@@ -798,8 +898,8 @@ const char* fp4q_status_string(fp4q_status status) {
   switch (status) {
     case FP4Q_OK: return "ok";
     case FP4Q_ERR_ARG: return "invalid argument";
-    case FP4Q_ERR_SHAPE: return "invalid shape (K must be a multiple of max(group, hadamard_block))";
-    case FP4Q_ERR_ALIGN: return "pointer not aligned (16 bytes for arrays, 4 for the tensor scale)";
+    case FP4Q_ERR_SHAPE: return "invalid shape (a size outside the call's shape rules)";
+    case FP4Q_ERR_ALIGN: return "pointer not aligned (16 bytes for arrays, 4 for fp32 scales)";
     case FP4Q_ERR_UNSUPPORTED: return "unsupported format / group / block / rule";
     case FP4Q_ERR_CUDA: return "CUDA error";
     case FP4Q_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";

@@ -54,11 +54,15 @@ struct KernelInfo {
 // Occupancy is computed for smem_bytes, the dynamic shared memory of the launch; the kernel
 // may be launched with up to max_smem_bytes (when larger), which every call for one kernel
 // passes alike.  Results are cached per (kernel, context, smem_bytes, threads).
-fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes);
+// carveout: the share of the unified L1 / shared storage kept as shared memory, in percent (-1:
+// the driver's choice, for kernels that stream through L1).
+fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes,
+                             int carveout = 100);
 
 template <class K>
-fp4q_status kernel_info(K kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes = 0) {
-  return kernel_info_impl(reinterpret_cast<const void*>(kernel), smem_bytes, threads, out, max_smem_bytes);
+fp4q_status kernel_info(K kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes = 0,
+                        int carveout = 100) {
+  return kernel_info_impl(reinterpret_cast<const void*>(kernel), smem_bytes, threads, out, max_smem_bytes, carveout);
 }
 
 // The butterfly kernels (rotate + quantize, error pass, amax) may stage a sign mask of up to
@@ -156,6 +160,15 @@ template <int FMT>
 fp4q_status launch_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_ts, const uint8_t* b_codes,
                         const uint8_t* b_scales, const float* b_ts, int64_t M, int64_t N, int64_t K, uint16_t* d,
                         cudaStream_t stream);
+// The 8-bit operators (fp4q_inst_fp8.cu, fp4q_inst_gemm_fp8.cu); arguments validated by the caller.
+fp4q_status launch_quantize_fp8(int scale_format, int dtype, int block_rows, const void* x, int64_t ldx, int64_t M,
+                                int64_t K, void* codes, void* scales, cudaStream_t stream);
+fp4q_status launch_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int64_t ldx, const void* residual,
+                                   int64_t ldr, const void* weight, float eps, int64_t M, int64_t K,
+                                   void* residual_out, int64_t ldo, void* codes, void* scales, cudaStream_t stream);
+fp4q_status launch_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
+                            const void* b_codes, const void* b_scales, int64_t M, int64_t N, int64_t K, void* d,
+                            cudaStream_t stream);
 fp4q_status launch_tensor_scale_finalize(const float* partials, int n, float* out, cudaStream_t stream);
 fp4q_status launch_quant_error_empty(const double* partials, double* out, cudaStream_t stream);
 // Device address of the no-allocation path's fixed scratch (kNoAllocMaxPartials floats).
@@ -174,6 +187,7 @@ fp4q_status status_mma_qe(unsigned int* v);
 fp4q_status launch_wait_timeout_selftest(cudaStream_t stream);
 fp4q_status status_dequant(unsigned int* v);
 fp4q_status status_gemm(unsigned int* v);
+fp4q_status status_gemm_fp8(unsigned int* v);
 
 }  // namespace host
 }  // namespace fp4q

@@ -26,10 +26,13 @@ FP4Q_MXFP4, FP4Q_NVFP4, FP4Q_MXFP4_MBS = 0, 1, 2
 FP4Q_KERNEL_AUTO, FP4Q_KERNEL_BUTTERFLY, FP4Q_KERNEL_TENSOR_CORE = 0, 1, 2
 (FP4Q_SCALE_FLOOR_OCP, FP4Q_SCALE_CEIL_NOCLIP, FP4Q_SCALE_OAS,
  FP4Q_SCALE_NV_STATIC, FP4Q_SCALE_NV_DYNAMIC) = range(5)
+FP4Q_FP8_SCALE_F32, FP4Q_FP8_SCALE_E8M0 = 0, 1
+FP4Q_DTYPE_BF16, FP4Q_DTYPE_FP16, FP4Q_DTYPE_F32 = 0, 1, 2
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 
 _SIGS = {
     "fp4q_plan_create": (_int, [ctypes.POINTER(_vp), _int, _int, _int, _int]),
@@ -45,6 +48,9 @@ _SIGS = {
     "fp4q_rotate_quantize_mbs": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "fp4q_dequantize_mbs": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _vp]),
     "fp4q_gemm": (_int, [_int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
+    "fp4q_quantize_fp8": (_int, [_int, _int, _int, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "fp4q_add_rmsnorm_fp8": (_int, [_int, _int, _vp, _i64, _vp, _i64, _vp, _f32, _i64, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "fp4q_gemm_fp8": (_int, [_int, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp4q_device_status": (_int, []),
     "fp4q_selftest_wait_timeout": (_int, [_vp]),
     "fp4q_status_string": (ctypes.c_char_p, [_int]),
@@ -193,6 +199,29 @@ def fp4q_gemm(fmt: int, a_codes, a_scales, a_tensor_scale, b_codes, b_scales, b_
                           _ptr(b_tensor_scale), M, N, K, _ptr(d_bf16), _stream(stream)), "fp4q_gemm")
 
 
+def fp4q_quantize_fp8(scale_format: int, dtype: int, block_rows: int, x, ldx: int, M: int, K: int, codes_out,
+                      scales_out, stream=None) -> None:
+    """E4M3 codes [M, K] and scales of x (rows ldx elements apart): block_rows 1 for a scale per row and
+    128 channels, 128 for a scale per 128 x 128 tile."""
+    _check(_lib.fp4q_quantize_fp8(scale_format, dtype, block_rows, _ptr(x), ldx, M, K, _ptr(codes_out),
+                                  _ptr(scales_out), _stream(stream)), "fp4q_quantize_fp8")
+
+
+def fp4q_add_rmsnorm_fp8(scale_format: int, dtype: int, x, ldx: int, residual, ldr: int, weight, eps: float, M: int,
+                         K: int, residual_out, ldo: int, codes_out, scales_out, stream=None) -> None:
+    """residual_out = x + residual, and E4M3 codes and scales (per row and 128 channels) of its RMS norm."""
+    _check(_lib.fp4q_add_rmsnorm_fp8(scale_format, dtype, _ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), eps, M, K,
+                                     _ptr(residual_out), ldo, _ptr(codes_out), _ptr(scales_out), _stream(stream)),
+           "fp4q_add_rmsnorm_fp8")
+
+
+def fp4q_gemm_fp8(scale_format: int, out_dtype: int, a_codes, a_scales, b_codes, b_scales, M: int, N: int, K: int, d,
+                  stream=None) -> None:
+    """D [M, N] = A B^T from the codes and scales of A [M, K] (block_rows 1) and B [N, K] (block_rows 128)."""
+    _check(_lib.fp4q_gemm_fp8(scale_format, out_dtype, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
+                              M, N, K, _ptr(d), _stream(stream)), "fp4q_gemm_fp8")
+
+
 def fp4q_device_status() -> int:
     return _lib.fp4q_device_status()
 
@@ -253,3 +282,121 @@ def quant_error(plan: Plan, x, tensor_scale=None, stream=None):
     fp4q_quant_error(plan, x, M, K, ts, out, stream)
     s, e, q = out.tolist()
     return s, e, q
+
+
+# ---- 8-bit linear layers.  Codes are torch.float8_e4m3fn tensors, scales float32 or torch.float8_e8m0fnu
+# ones.  The calls run on the tensors' device, on its current stream unless one is given.
+
+def _fp8_dtypes():
+    import torch
+    return ({torch.bfloat16: FP4Q_DTYPE_BF16, torch.float16: FP4Q_DTYPE_FP16, torch.float32: FP4Q_DTYPE_F32},
+            {FP4Q_FP8_SCALE_F32: torch.float32, FP4Q_FP8_SCALE_E8M0: torch.float8_e8m0fnu})
+
+
+def _fp8_rows(name: str, t, shape=None, dtype=None, device=None) -> int:
+    """Check a 2-D tensor of rows whose elements are neighbours; returns the distance between rows."""
+    import torch
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float16) or \
+            (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D bf16 or fp16 CUDA tensor whose rows are contiguous")
+    if (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype) or \
+            (device is not None and t.device != device):
+        raise ValueError(f"{name} must match x in shape, dtype and device")
+    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+
+
+def _fp8_buffer(name: str, t, shape, dtype, device):
+    """A given output after checking it, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _on_device(device, stream, call):
+    """call(raw stream) with `device` current."""
+    import torch
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if torch.cuda.current_device() == device.index:
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def quantize_fp8(x, block_rows: int = 1, scale_format: int = FP4Q_FP8_SCALE_F32, codes=None, scales=None, stream=None):
+    """x: bf16 or fp16 CUDA tensor [M, K] (K a multiple of 16; rows may be strided) -> (codes
+    float8_e4m3fn [M, K], scales).  block_rows 1: scales [M, ceil(K / 128)], for activations; 128:
+    [ceil(M / 128), ceil(K / 128)], for weights.  scale_format: FP4Q_FP8_SCALE_F32 (float32 scales) or
+    FP4Q_FP8_SCALE_E8M0 (float8_e8m0fnu).  codes, scales: outputs to write into."""
+    import torch
+    dtypes, scale_dtypes = _fp8_dtypes()
+    ldx = _fp8_rows("x", x)
+    if block_rows not in (1, 128) or scale_format not in scale_dtypes:
+        raise ValueError("block_rows must be 1 or 128 and scale_format one of FP4Q_FP8_SCALE_*")
+    M, K = x.shape
+    codes = _fp8_buffer("codes", codes, (M, K), torch.float8_e4m3fn, x.device)
+    scales = _fp8_buffer("scales", scales, (-(-M // block_rows), -(-K // 128)), scale_dtypes[scale_format], x.device)
+    _on_device(x.device, stream, lambda s: fp4q_quantize_fp8(scale_format, dtypes[x.dtype], block_rows, x, ldx, M, K,
+                                                             codes, scales, s))
+    return codes, scales
+
+
+def add_rmsnorm_fp8(x, residual, weight, eps: float, scale_format: int = FP4Q_FP8_SCALE_F32, residual_out=None,
+                    codes=None, scales=None, stream=None):
+    """h = x + residual (residual None: x alone), y = h / sqrt(mean(h^2) + eps) * weight -> (codes
+    float8_e4m3fn [M, K] and scales [M, ceil(K / 128)] of y, residual_out = h in x's dtype or None).
+    x, residual [M, K] and weight [K]: bf16 or fp16, of one dtype; rows may be strided.  residual_out may
+    be given: residual or x itself, or another tensor that overlaps neither."""
+    import torch
+    dtypes, scale_dtypes = _fp8_dtypes()
+    ldx = _fp8_rows("x", x)
+    M, K = x.shape
+    if scale_format not in scale_dtypes:
+        raise ValueError("scale_format must be one of FP4Q_FP8_SCALE_*")
+    if weight.shape != (K,) or weight.dtype != x.dtype or weight.device != x.device or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous tensor [K] of x's dtype and device")
+    ldr = ldo = K
+    if residual is not None:
+        ldr = _fp8_rows("residual", residual, x.shape, x.dtype, x.device)
+        if residual_out is None:
+            residual_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
+        ldo = _fp8_rows("residual_out", residual_out, x.shape, x.dtype, x.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out goes with a residual")
+    codes = _fp8_buffer("codes", codes, (M, K), torch.float8_e4m3fn, x.device)
+    scales = _fp8_buffer("scales", scales, (M, -(-K // 128)), scale_dtypes[scale_format], x.device)
+    _on_device(x.device, stream, lambda s: fp4q_add_rmsnorm_fp8(scale_format, dtypes[x.dtype], x, ldx, residual, ldr,
+                                                                weight, eps, M, K, residual_out, ldo, codes, scales,
+                                                                s))
+    return codes, scales, residual_out
+
+
+def gemm_fp8(a_codes, a_scales, b_codes, b_scales, out_dtype=None, out=None, stream=None):
+    """D = A B^T [M, N] from A's codes [M, K] and scales [M, ceil(K / 128)] (quantize_fp8 or
+    add_rmsnorm_fp8) and B's codes [N, K] and scales [ceil(N / 128), ceil(K / 128)] (quantize_fp8 with
+    block_rows 128); both scales float32 or both float8_e8m0fnu.  out_dtype: bf16 (the default), fp16 or
+    fp32.  out: a tensor to write into."""
+    import torch
+    dtypes, scale_dtypes = _fp8_dtypes()
+    device = a_codes.device
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
+        raise ValueError("a_codes [M, K] and b_codes [N, K] must be 2-D with the same K")
+    (M, K), N = a_codes.shape, b_codes.shape[0]
+    kb = -(-K // 128)
+    for name, t, shape, types in (("a_codes", a_codes, (M, K), (torch.float8_e4m3fn,)),
+                                  ("b_codes", b_codes, (N, K), (torch.float8_e4m3fn,)),
+                                  ("a_scales", a_scales, (M, kb), tuple(scale_dtypes.values())),
+                                  ("b_scales", b_scales, (-(-N // 128), kb), (a_scales.dtype,))):
+        if t.shape != shape or t.dtype not in types or t.device != device or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {shape}, one of {types}, on {device}")
+    out_dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    if out_dtype not in dtypes:
+        raise ValueError("out_dtype must be bf16, fp16 or fp32")
+    out = _fp8_buffer("out", out, (M, N), out_dtype, device)
+    fmt = FP4Q_FP8_SCALE_F32 if a_scales.dtype == torch.float32 else FP4Q_FP8_SCALE_E8M0
+    _on_device(device, stream, lambda s: fp4q_gemm_fp8(fmt, dtypes[out_dtype], a_codes, a_scales, b_codes, b_scales, M,
+                                                       N, K, out, s))
+    return out
