@@ -285,45 +285,67 @@ def quant_error(plan: Plan, x, tensor_scale=None, stream=None):
 
 
 # ---- 8-bit linear layers.  Codes are torch.float8_e4m3fn tensors, scales float32 or torch.float8_e8m0fnu
-# ones.  The calls run on the tensors' device, on its current stream unless one is given.
+# ones.  The calls run on the tensors' device, on its current stream unless one is given.  The checks are
+# kept short: at one token a call costs the host more than it costs the GPU.
 
-def _fp8_dtypes():
+_torch = None            # set by the first call: importing this module does not import torch
+_fp8_dtype_codes: dict = {}
+_fp8_scale_dtypes: dict = {}
+
+
+def _fp8_init() -> None:
+    global _torch
     import torch
-    return ({torch.bfloat16: FP4Q_DTYPE_BF16, torch.float16: FP4Q_DTYPE_FP16, torch.float32: FP4Q_DTYPE_F32},
-            {FP4Q_FP8_SCALE_F32: torch.float32, FP4Q_FP8_SCALE_E8M0: torch.float8_e8m0fnu})
+    _fp8_dtype_codes.update({torch.bfloat16: FP4Q_DTYPE_BF16, torch.float16: FP4Q_DTYPE_FP16,
+                             torch.float32: FP4Q_DTYPE_F32})
+    _fp8_scale_dtypes.update({FP4Q_FP8_SCALE_F32: torch.float32, FP4Q_FP8_SCALE_E8M0: torch.float8_e8m0fnu})
+    _torch = torch
 
 
-def _fp8_rows(name: str, t, shape=None, dtype=None, device=None) -> int:
-    """Check a 2-D tensor of rows whose elements are neighbours; returns the distance between rows."""
-    import torch
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float16) or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
+def _fp8_rows(name: str, t, like=None) -> int:
+    """Check a 2-D tensor of rows whose elements are neighbours, and against x (like) if one is given;
+    returns the distance between rows."""
+    shape, ld = t.shape, 0
+    if t.is_cuda and len(shape) == 2 and _fp8_dtype_codes.get(t.dtype, FP4Q_DTYPE_F32) != FP4Q_DTYPE_F32:
+        if shape[0] <= 1 or shape[1] == 0:
+            ld = shape[1]
+        else:
+            ld = t.stride(0)
+        if shape[1] > 1 and t.stride(1) != 1:
+            ld = -1
+    else:
+        ld = -1
+    if ld < 0:
         raise ValueError(f"{name} must be a 2-D bf16 or fp16 CUDA tensor whose rows are contiguous")
-    if (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype) or \
-            (device is not None and t.device != device):
+    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{name} must match x in shape, dtype and device")
-    return t.stride(0) if t.shape[0] > 1 and t.shape[1] > 0 else t.shape[1]
+    return ld
 
 
 def _fp8_buffer(name: str, t, shape, dtype, device):
     """A given output after checking it, or a new one."""
-    import torch
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _torch.empty(shape, dtype=dtype, device=device)
     if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
 
-def _on_device(device, stream, call):
-    """call(raw stream) with `device` current."""
-    import torch
-    if stream is not None and not isinstance(stream, int) and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    if torch.cuda.current_device() == device.index:
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+def _fp8_call(name: str, device, stream, *args) -> None:
+    """The C call `name` on the device's current stream, or on the given one, with the device current."""
+    index = device.index
+    if stream is None:
+        stream = _torch._C._cuda_getCurrentRawStream(index)   # current_stream() takes 3 us to say the same
+    elif not isinstance(stream, int):
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        stream = stream.cuda_stream
+    if _torch.cuda.current_device() == index:
+        status = getattr(_lib, name)(*args, stream)
+    else:
+        with _torch.cuda.device(index):
+            status = getattr(_lib, name)(*args, stream)
+    _check(status, name)
 
 
 def quantize_fp8(x, block_rows: int = 1, scale_format: int = FP4Q_FP8_SCALE_F32, codes=None, scales=None, stream=None):
@@ -331,16 +353,17 @@ def quantize_fp8(x, block_rows: int = 1, scale_format: int = FP4Q_FP8_SCALE_F32,
     float8_e4m3fn [M, K], scales).  block_rows 1: scales [M, ceil(K / 128)], for activations; 128:
     [ceil(M / 128), ceil(K / 128)], for weights.  scale_format: FP4Q_FP8_SCALE_F32 (float32 scales) or
     FP4Q_FP8_SCALE_E8M0 (float8_e8m0fnu).  codes, scales: outputs to write into."""
-    import torch
-    dtypes, scale_dtypes = _fp8_dtypes()
+    if _torch is None:
+        _fp8_init()
     ldx = _fp8_rows("x", x)
-    if block_rows not in (1, 128) or scale_format not in scale_dtypes:
+    if block_rows not in (1, 128) or scale_format not in _fp8_scale_dtypes:
         raise ValueError("block_rows must be 1 or 128 and scale_format one of FP4Q_FP8_SCALE_*")
     M, K = x.shape
-    codes = _fp8_buffer("codes", codes, (M, K), torch.float8_e4m3fn, x.device)
-    scales = _fp8_buffer("scales", scales, (-(-M // block_rows), -(-K // 128)), scale_dtypes[scale_format], x.device)
-    _on_device(x.device, stream, lambda s: fp4q_quantize_fp8(scale_format, dtypes[x.dtype], block_rows, x, ldx, M, K,
-                                                             codes, scales, s))
+    device = x.device
+    codes = _fp8_buffer("codes", codes, (M, K), _torch.float8_e4m3fn, device)
+    scales = _fp8_buffer("scales", scales, (-(-M // block_rows), -(-K // 128)), _fp8_scale_dtypes[scale_format], device)
+    _fp8_call("fp4q_quantize_fp8", device, stream, scale_format, _fp8_dtype_codes[x.dtype], block_rows, x.data_ptr(),
+              ldx, M, K, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -350,27 +373,31 @@ def add_rmsnorm_fp8(x, residual, weight, eps: float, scale_format: int = FP4Q_FP
     float8_e4m3fn [M, K] and scales [M, ceil(K / 128)] of y, residual_out = h in x's dtype or None).
     x, residual [M, K] and weight [K]: bf16 or fp16, of one dtype; rows may be strided.  residual_out may
     be given: residual or x itself, or another tensor that overlaps neither."""
-    import torch
-    dtypes, scale_dtypes = _fp8_dtypes()
+    if _torch is None:
+        _fp8_init()
     ldx = _fp8_rows("x", x)
     M, K = x.shape
-    if scale_format not in scale_dtypes:
+    device, dtype = x.device, x.dtype
+    if scale_format not in _fp8_scale_dtypes:
         raise ValueError("scale_format must be one of FP4Q_FP8_SCALE_*")
-    if weight.shape != (K,) or weight.dtype != x.dtype or weight.device != x.device or not weight.is_contiguous():
+    if weight.shape != (K,) or weight.dtype != dtype or weight.device != device or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous tensor [K] of x's dtype and device")
     ldr = ldo = K
+    p_res = p_out = None
     if residual is not None:
-        ldr = _fp8_rows("residual", residual, x.shape, x.dtype, x.device)
+        ldr = _fp8_rows("residual", residual, x)
         if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=x.dtype, device=x.device)
-        ldo = _fp8_rows("residual_out", residual_out, x.shape, x.dtype, x.device)
+            residual_out = _torch.empty((M, K), dtype=dtype, device=device)
+        else:
+            ldo = _fp8_rows("residual_out", residual_out, x)
+        p_res, p_out = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out goes with a residual")
-    codes = _fp8_buffer("codes", codes, (M, K), torch.float8_e4m3fn, x.device)
-    scales = _fp8_buffer("scales", scales, (M, -(-K // 128)), scale_dtypes[scale_format], x.device)
-    _on_device(x.device, stream, lambda s: fp4q_add_rmsnorm_fp8(scale_format, dtypes[x.dtype], x, ldx, residual, ldr,
-                                                                weight, eps, M, K, residual_out, ldo, codes, scales,
-                                                                s))
+    codes = _fp8_buffer("codes", codes, (M, K), _torch.float8_e4m3fn, device)
+    scales = _fp8_buffer("scales", scales, (M, -(-K // 128)), _fp8_scale_dtypes[scale_format], device)
+    if M * K > 0:   # (an empty tensor's null pointers say nothing about a residual)
+        _fp8_call("fp4q_add_rmsnorm_fp8", device, stream, scale_format, _fp8_dtype_codes[dtype], x.data_ptr(), ldx,
+                  p_res, ldr, weight.data_ptr(), eps, M, K, p_out, ldo, codes.data_ptr(), scales.data_ptr())
     return codes, scales, residual_out
 
 
@@ -379,24 +406,28 @@ def gemm_fp8(a_codes, a_scales, b_codes, b_scales, out_dtype=None, out=None, str
     add_rmsnorm_fp8) and B's codes [N, K] and scales [ceil(N / 128), ceil(K / 128)] (quantize_fp8 with
     block_rows 128); both scales float32 or both float8_e8m0fnu.  out_dtype: bf16 (the default), fp16 or
     fp32.  out: a tensor to write into."""
-    import torch
-    dtypes, scale_dtypes = _fp8_dtypes()
-    device = a_codes.device
-    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
-        raise ValueError("a_codes [M, K] and b_codes [N, K] must be 2-D with the same K")
+    if _torch is None:
+        _fp8_init()
+    device, s_dtype = a_codes.device, a_scales.dtype
+    if a_codes.dim() != 2 or b_codes.dim() != 2:
+        raise ValueError("a_codes [M, K] and b_codes [N, K] must be 2-D")
     (M, K), N = a_codes.shape, b_codes.shape[0]
     kb = -(-K // 128)
-    for name, t, shape, types in (("a_codes", a_codes, (M, K), (torch.float8_e4m3fn,)),
-                                  ("b_codes", b_codes, (N, K), (torch.float8_e4m3fn,)),
-                                  ("a_scales", a_scales, (M, kb), tuple(scale_dtypes.values())),
-                                  ("b_scales", b_scales, (-(-N // 128), kb), (a_scales.dtype,))):
-        if t.shape != shape or t.dtype not in types or t.device != device or not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {shape}, one of {types}, on {device}")
-    out_dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
-    if out_dtype not in dtypes:
+    fmt = FP4Q_FP8_SCALE_F32 if s_dtype == _torch.float32 else FP4Q_FP8_SCALE_E8M0
+    if s_dtype != _fp8_scale_dtypes[fmt]:
+        raise ValueError("the scales must be float32 or float8_e8m0fnu")
+    if not a_codes.is_cuda:
+        raise ValueError("the operands must be CUDA tensors")
+    e4m3 = _torch.float8_e4m3fn
+    _fp8_buffer("a_codes", a_codes, (M, K), e4m3, device)
+    _fp8_buffer("b_codes", b_codes, (N, K), e4m3, device)
+    _fp8_buffer("a_scales", a_scales, (M, kb), s_dtype, device)
+    _fp8_buffer("b_scales", b_scales, (-(-N // 128), kb), s_dtype, device)
+    if out_dtype is None:
+        out_dtype = _torch.bfloat16 if out is None else out.dtype
+    if out_dtype not in _fp8_dtype_codes:
         raise ValueError("out_dtype must be bf16, fp16 or fp32")
     out = _fp8_buffer("out", out, (M, N), out_dtype, device)
-    fmt = FP4Q_FP8_SCALE_F32 if a_scales.dtype == torch.float32 else FP4Q_FP8_SCALE_E8M0
-    _on_device(device, stream, lambda s: fp4q_gemm_fp8(fmt, dtypes[out_dtype], a_codes, a_scales, b_codes, b_scales, M,
-                                                       N, K, out, s))
+    _fp8_call("fp4q_gemm_fp8", device, stream, fmt, _fp8_dtype_codes[out_dtype], a_codes.data_ptr(),
+              a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), M, N, K, out.data_ptr())
     return out
