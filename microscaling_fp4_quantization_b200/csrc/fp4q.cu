@@ -19,20 +19,21 @@ namespace host {
 namespace {
 thread_local char g_last_cuda_error[kLastErrorBytes] = "";
 std::mutex g_ctx_mu;
-// kernel, context, the dynamic shared memory occupancy is computed for, threads per CTA
+// kernel, context, the dynamic shared memory occupancy is computed for, threads per CTA, CTAs per cluster
 struct InfoKey {
   const void* kernel;
   uint64_t ctx;
-  int smem, threads;
+  int smem, threads, cluster;
   bool operator==(const InfoKey& o) const {
-    return kernel == o.kernel && ctx == o.ctx && smem == o.smem && threads == o.threads;
+    return kernel == o.kernel && ctx == o.ctx && smem == o.smem && threads == o.threads && cluster == o.cluster;
   }
 };
 struct InfoKeyHash {
   size_t operator()(const InfoKey& k) const {
     uint64_t h = reinterpret_cast<uint64_t>(k.kernel) * 0x9E3779B97F4A7C15ull;
     h ^= k.ctx + 0x632BE59BD9B4E019ull + (h << 6) + (h >> 2);
-    h ^= (static_cast<uint64_t>(static_cast<uint32_t>(k.smem)) << 20) ^ static_cast<uint64_t>(k.threads);
+    h ^= (static_cast<uint64_t>(static_cast<uint32_t>(k.smem)) << 20) ^ static_cast<uint64_t>(k.threads) ^
+         (static_cast<uint64_t>(k.cluster) << 12);
     return static_cast<size_t>(h);
   }
 };
@@ -95,7 +96,7 @@ fp4q_status bound_context_id(uint64_t* out) {
 }
 
 fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes,
-                             int carveout) {
+                             int carveout, int cluster) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -103,7 +104,7 @@ fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, Ke
   uint64_t ctx = 0;
   fp4q_status st = bound_context_id(&ctx);
   if (st != FP4Q_OK) return st;
-  const InfoKey key{kernel, ctx, smem_bytes, threads};
+  const InfoKey key{kernel, ctx, smem_bytes, threads, cluster};
   std::lock_guard<std::mutex> lk(g_info_mu);
   auto it = g_info.find(key);
   if (it != g_info.end()) {
@@ -121,6 +122,22 @@ fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, Ke
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ki.ctas_per_sm, kernel, threads, smem_bytes);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveBlocksPerMultiprocessor");
   if (ki.ctas_per_sm < 1) ki.ctas_per_sm = 1;
+  if (cluster > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&ki.max_clusters, kernel, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+    if (ki.max_clusters < 1) ki.max_clusters = 1;
+  }
   g_info[key] = ki;
   *out = ki;
   return FP4Q_OK;

@@ -29,6 +29,7 @@ struct GemmFp8Args {
   int64_t M, N;
   int kb;                 // K-blocks
   int tiles_m, tiles_n;
+  int sf_vec;             // E8M0 scales: rows start on whole words
   int vec;                // D's rows keep a 32-byte (2), 16-byte (1) or no (0) alignment
 };
 
@@ -40,43 +41,68 @@ __device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t da, uint64_t
       : "memory");
 }
 
+__device__ __forceinline__ void umma_e4m3_scaled(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc,
+                                                 uint32_t tsfa, uint32_t tsfb, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n}" ::"r"(tmem_d),
+      "l"(da), "l"(db), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb)
+      : "memory");
+}
+
 // E4M3 x E4M3 (format 0), K-major, fp32 accumulator, N >> 3, M >> 4.
 constexpr uint32_t gemm_fp8_idesc(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// 32 / 16 TMEM columns of this thread's lane as packed pairs; the values are there after tmem_wait_*.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 / 8 TMEM columns of this thread's lane, waited for, as pairs: a load's registers are neighbours, so
+// pairing them in the same statement costs no moves, which pairing them outside it did.
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, f32x2 (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
+      "{\n .reg .b32 t<16>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x16.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15}, [%8];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {t0, t1};\n"
+      " mov.b64 %1, {t2, t3};\n"
+      " mov.b64 %2, {t4, t5};\n"
+      " mov.b64 %3, {t6, t7};\n"
+      " mov.b64 %4, {t8, t9};\n"
+      " mov.b64 %5, {t10, t11};\n"
+      " mov.b64 %6, {t12, t13};\n"
+      " mov.b64 %7, {t14, t15};\n"
+      "}"
+      : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3]), "=l"(r[4]), "=l"(r[5]), "=l"(r[6]), "=l"(r[7])
+      : "r"(taddr)
+      : "memory");
 }
-__device__ __forceinline__ void tmem_ld16_bits(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_pairs(uint32_t taddr, f32x2 (&r)[4]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+      "{\n .reg .b32 t<8>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x8.b32 {t0,t1,t2,t3,t4,t5,t6,t7}, [%4];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {t0, t1};\n"
+      " mov.b64 %1, {t2, t3};\n"
+      " mov.b64 %2, {t4, t5};\n"
+      " mov.b64 %3, {t6, t7};\n"
+      "}"
+      : "=l"(r[0]), "=l"(r[1]), "=l"(r[2]), "=l"(r[3])
+      : "r"(taddr)
+      : "memory");
 }
-// The wait ties the registers to it, so that nothing reads them before.
-template <int N>
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[N]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
 }
 
+// E8M0 byte -> fp32: 0 is 2^-127 (a subnormal), 255 NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
+}
 template <int SF>
 __device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
   if constexpr (SF == kSfF32) return __ldg(static_cast<const float*>(scales) + i);
-  const uint32_t b = __ldg(static_cast<const uint8_t*>(scales) + i);
-  // byte 0 is 2^-127 (a subnormal), 255 NaN
-  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
+  return e8m0_value(__ldg(static_cast<const uint8_t*>(scales) + i));
 }
 
 template <int OT>
@@ -89,206 +115,396 @@ __device__ __forceinline__ void store_one(void* d, int64_t i, float v) {
     static_cast<uint16_t*>(d)[i] = static_cast<uint16_t>(pair_from_f32<kDtFp16>(v, 0.0f) & 0xFFFFu);
 }
 
-// Sixteen neighbouring columns of one row of D, as far as they exist.
+// Sixteen / eight neighbouring columns of one row of D, as far as they exist.
+template <int OT, int N>
+__device__ __forceinline__ void store_row_tail(const GemmFp8Args& g, int64_t row, int64_t col, const f32x2* acc) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    float lo, hi;
+    f2_unpack(acc[i], lo, hi);
+    if (col + 2 * i < g.N) store_one<OT>(g.d, row * g.N + col + 2 * i, lo);
+    if (col + 2 * i + 1 < g.N) store_one<OT>(g.d, row * g.N + col + 2 * i + 1, hi);
+  }
+}
+template <int OT>
+__device__ __forceinline__ void store_row8(const GemmFp8Args& g, int64_t row, int64_t col, const f32x2* acc) {
+  if (g.vec == 0 || col + 8 > g.N) {
+    store_row_tail<OT, 8>(g, row, col, acc);
+  } else if constexpr (OT == kDtF32) {
+    float* p = static_cast<float*>(g.d) + row * g.N + col;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      float v[4];
+      f2_unpack(acc[i], v[0], v[1]);
+      f2_unpack(acc[i + 1], v[2], v[3]);
+      stg128(p + 2 * i, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
+  } else {
+    stg128(static_cast<uint16_t*>(g.d) + row * g.N + col, pair_from_f32<OT>(acc[0]), pair_from_f32<OT>(acc[1]),
+           pair_from_f32<OT>(acc[2]), pair_from_f32<OT>(acc[3]));
+  }
+}
 template <int OT>
 __device__ __forceinline__ void store_row16(const GemmFp8Args& g, int64_t row, int64_t col, const f32x2* acc) {
-  const int64_t at = row * g.N + col;
   if (g.vec == 0 || col + 16 > g.N) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float lo, hi;
-      f2_unpack(acc[i], lo, hi);
-      if (col + 2 * i < g.N) store_one<OT>(g.d, at + 2 * i, lo);
-      if (col + 2 * i + 1 < g.N) store_one<OT>(g.d, at + 2 * i + 1, hi);
-    }
-    return;
-  }
-  if constexpr (OT == kDtF32) {
-    float* p = static_cast<float*>(g.d) + at;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float lo, hi;
-      f2_unpack(acc[i], lo, hi);
-      w[2 * i] = __float_as_uint(lo), w[2 * i + 1] = __float_as_uint(hi);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) stg128(p + i, w[i], w[i + 1], w[i + 2], w[i + 3]);
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(g.d) + at;
+    store_row_tail<OT, 16>(g, row, col, acc);
+  } else if (OT != kDtF32 && g.vec == 2) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pair_from_f32<OT>(acc[i]);
-    if (g.vec == 2) {
-      stg256(p, w);   // whole 32-byte sectors
-    } else {
-      stg128(p, w[0], w[1], w[2], w[3]);
-      stg128(p + 8, w[4], w[5], w[6], w[7]);
-    }
+    for (int i = 0; i < 8; ++i) w[i] = pair_from_f32<OT == kDtF32 ? kDtBf16 : OT>(acc[i]);
+    stg256(static_cast<uint16_t*>(g.d) + row * g.N + col, w);   // whole 32-byte sectors
+  } else {
+    store_row8<OT>(g, row, col, acc);
+    store_row8<OT>(g, row, col + 8, acc + 4);
   }
 }
 
-// ---------------------------------------------------------------- many rows: tiles of 128 x BN
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync_all() {
+  cluster_arrive();
+  cluster_wait();
+}
+// The address of `addr` (of this CTA's shared memory) in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// Arrive on a barrier of another CTA of the cluster.  What it announces is that tensor memory has been
+// read, which tcgen05's own fences order: a release at cluster scope took 500 ns of every block.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// Four floats of shared memory as two pairs.
+__device__ __forceinline__ void lds_pairs(uint32_t addr, f32x2& a, f32x2& b) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
+
+// ---------------------------------------------------------------- many rows: tiles of 128 C x BN
 //
 // A is the MMA's row operand, so a thread of the adding warps holds one row of D and half the tile's
 // columns: its multiplier is one number a block, sa[row][j] * sb[n / 128][j], and a block costs it
-// one fused multiply-add per element.  Persistent CTAs, one per SM, round-robin over the tiles.
-template <int BN_, int OT, int SF>
+// one fused multiply-add per element.  Persistent, round-robin over the tiles.  C = 2 pairs the CTAs
+// of a cluster on one tile (cta_group::2, M = 256): each loads its 128 rows of A and half of B's, and
+// the leader issues the MMAs of both.
+constexpr int kMmaTries = 64;   // times an MMA warp asks for its barriers before it suspends
+
+template <int CTAS, int BN_, int OT, int SF>
 struct GemmFp8Config {
-  static constexpr int kBM = 128, kBN = BN_, kBK = kFp8Block;
+  static constexpr int kCtas = CTAS;
+  static constexpr int kBM = 128 * CTAS, kBN = BN_, kBK = kFp8Block;
   static constexpr int kOut = OT, kSf = SF;
-  static constexpr int kABytes = kBM * kBK, kBBytes = kBN * kBK;
+  static constexpr int kARows = 128, kBRows = kBN / CTAS;   // a CTA's share of a stage
+  static constexpr int kABytes = kARows * kBK, kBBytes = kBRows * kBK;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kBN == 256 ? 4 : 6;
+  static constexpr int kStages = (196 * 1024) / kStageBytes;
   static constexpr int kBarOffset = kStages * kStageBytes;
   static constexpr int kSmemBytes = 1024 + kBarOffset + 256;
-  static constexpr int kTmemCols = 2 * kBN;                 // two accumulators
-  static constexpr int kAddWarps = 8, kAddWarp0 = 2;        // two per TMEM lane quarter
+  static constexpr int kAccs = 512 / kBN;                   // accumulators in tensor memory
+  static constexpr int kTmemCols = kAccs * kBN;
+  static constexpr int kAddWarp0 = 4, kAddWarps = 8;        // two per TMEM lane quarter
   static constexpr int kCols = kBN / 2;                     // columns per adding warp
   static constexpr int kThreads = 32 * (kAddWarp0 + kAddWarps);
+  // 128 sums a thread need more registers than 384 threads share out evenly (168): the first four
+  // warps hand theirs to the adding warps
+  static constexpr bool kRegSplit = kCols == 128;
+  static constexpr int kRegsLaunch = 168, kRegsFew = 40, kRegsMany = 232;
+  static_assert(kRegsFew * kAddWarp0 + kRegsMany * kAddWarps <= kRegsLaunch * (kAddWarp0 + kAddWarps));
   static constexpr uint32_t kIdesc = gemm_fp8_idesc(kBM, kBN);
 };
+
+// A position in a ring of N barriers: the slot, and the parity of the pass over the ring (kept rather
+// than worked out from a count: the MMA warp's loop has to stay shorter than the MMAs it issues).
+template <int N>
+struct RingPos {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Whether the phase is complete, asked once.  Asking takes some 90 cycles to a branch on the answer (a
+// wait that may suspend, 130), so the MMA warps ask for a block's barriers before they issue the block
+// in front of it, and wait only where the answer was no.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Two phases at once.
+__device__ __forceinline__ bool mbar_test2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+      " and.pred p, p, q;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar_a), "r"(parity_a), "r"(bar_b), "r"(parity_b)
+      : "memory");
+  return ok != 0;
+}
+
+// Wait of a whole converged warp: ask up to `tries` times, then wait; false when the wait ran out.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int tries) {
+#pragma unroll 1
+  for (int i = 0; i < tries; ++i)
+    if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity));
+}
+__device__ __forceinline__ bool warp_wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b, int tries) {
+#pragma unroll 1
+  for (int i = 0; i < tries; ++i)
+    if (__all_sync(0xFFFFFFFFu, mbar_test2(bar_a, parity_a, bar_b, parity_b))) return true;
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_a, parity_a) && mbar_wait_bounded(bar_b, parity_b));
+}
+
+template <int CTAS>
+__device__ __forceinline__ void gemm_fp8_mma(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+  if constexpr (CTAS == 1) {
+    umma_e4m3(tmem_d, da, db, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(tmem_d),
+        "l"(da), "l"(db), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+// Arrive on the barrier at this address, in both CTAs of a pair, when the MMAs issued so far are done.
+template <int CTAS>
+__device__ __forceinline__ void gemm_fp8_commit(uint32_t bar) {
+  if constexpr (CTAS == 1) {
+    umma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  }
+}
+// A box into this CTA's shared memory; a pair's copies complete on the leader's barrier.
+template <int CTAS>
+__device__ __forceinline__ void gemm_fp8_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  if constexpr (CTAS == 1) {
+    tma_load_2d(dst, map, x, y, bar);
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  }
+}
+
+// Producer warp of the many-row kernels: this CTA's rows of A and of B, stage after stage (one lane).
+// full barriers lie at `bars`, empty ones behind them; a pair's copies complete on the leader's.
+template <class Cfg>
+__device__ __forceinline__ void gemm_fp8_produce(const GemmFp8Args& g, const CUtensorMap& amap, const CUtensorMap& bmap,
+                                                 int rank, int t0, int dt, uint32_t stage0, uint32_t bars) {
+  constexpr int S = Cfg::kStages, C = Cfg::kCtas;
+  if ((threadIdx.x & 31) != 0) return;
+  pdl_wait();
+  const int n_tiles = g.tiles_m * g.tiles_n;
+  RingPos<S> r;
+  bool ok = true;
+  int filled = 0;
+  for (int t = t0; ok && t < n_tiles; t += dt) {
+    const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+    const int ra = tm * Cfg::kBM + rank * Cfg::kARows, rb = tn * Cfg::kBN + rank * Cfg::kBRows;
+    for (int j = 0; j < g.kb; ++j, r.next()) {
+      const uint32_t full = bars + 8u * r.i, empty = bars + 8u * (S + r.i), dst = stage0 + r.i * Cfg::kStageBytes;
+      if (!mbar_test(empty, r.parity ^ 1u) && !mbar_wait_bounded(empty, r.parity ^ 1u)) {
+        ok = false;
+        break;
+      }
+      if (rank == 0) mbar_arrive_expect_tx(full, C * Cfg::kStageBytes);
+      const uint32_t bar = C == 2 ? cluster_map(full, 0) : full;
+      gemm_fp8_load<C>(dst, &amap, j * Cfg::kBK, ra, bar);
+      gemm_fp8_load<C>(dst + Cfg::kABytes, &bmap, j * Cfg::kBK, rb, bar);
+      filled = filled < S ? filled + 1 : S;
+    }
+  }
+  // every issued copy has landed once its stage was read (or, where a wait ran out, long before): the
+  // ring's slots, from the oldest on
+  if (filled < S) r = RingPos<S>{};
+  for (int j = 0; j < filled; ++j, r.next())
+    mbar_wait_bounded(bars + 8u * (S + r.i), filled < S ? 0u : r.parity ^ 1u);
+}
 
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::kThreads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, GemmFp8Args g) {
-  constexpr int S = Cfg::kStages, BN = Cfg::kBN;
+  constexpr int S = Cfg::kStages, BN = Cfg::kBN, C = Cfg::kCtas, NA = Cfg::kAccs;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = C == 2 ? static_cast<int>(cluster_rank()) : 0;
   const uint32_t stage0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = stage0 + Cfg::kBarOffset;
   auto a_tile = [&](int s) { return stage0 + s * Cfg::kStageBytes; };
   auto b_tile = [&](int s) { return stage0 + s * Cfg::kStageBytes + Cfg::kABytes; };
-  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto full_bar = [&](int s) { return bars + 8u * s; };                  // a pair uses the leader's
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
   auto acc_full = [&](int d) { return bars + 8u * (2 * S + d); };
-  auto acc_empty = [&](int d) { return bars + 8u * (2 * S + 2 + d); };
+  auto acc_empty = [&](int d) { return bars + 8u * (2 * S + NA + d); };   // a pair uses the leader's
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int d = 0; d < 2; ++d) {
+    for (int d = 0; d < NA; ++d) {
       mbar_init(acc_full(d), 1);
-      mbar_init(acc_empty(d), Cfg::kAddWarps);
+      mbar_init(acc_empty(d), C * Cfg::kAddWarps);
     }
     fence_mbar_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem_base)),
-                 "r"(Cfg::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (C == 1) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem_base)),
+                   "r"(Cfg::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem_base)),
+                   "r"(Cfg::kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (C == 2) cluster_sync_all();   // the pair's barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   const int n_tiles = g.tiles_m * g.tiles_n;
+  const int t0 = static_cast<int>(blockIdx.x) / C, dt = static_cast<int>(gridDim.x) / C;
+  if constexpr (Cfg::kRegSplit)
+    if (warp < Cfg::kAddWarp0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsFew));
 
   if (warp == 0) {
-    // ---------------- producer
-    if (lane == 0) {
-      pdl_wait();
-      int64_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
-        const int tm = t % g.tiles_m, tn = t / g.tiles_m;
-        for (int j = 0; j < g.kb; ++j, ++it) {
-          const int s = static_cast<int>(it % S);
-          if (!mbar_wait_bounded(empty_bar(s), static_cast<uint32_t>((it / S) & 1) ^ 1u)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(full_bar(s), Cfg::kStageBytes);
-          tma_load_2d(a_tile(s), &amap, j * Cfg::kBK, tm * Cfg::kBM, full_bar(s));
-          tma_load_2d(b_tile(s), &bmap, j * Cfg::kBK, tn * BN, full_bar(s));
-        }
-      }
-      // let every issued copy land before the CTA can leave
-      for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
-        mbar_wait_bounded(full_bar(static_cast<int>(j % S)), static_cast<uint32_t>((j / S) & 1));
-    }
+    gemm_fp8_produce<Cfg>(g, amap, bmap, rank, t0, dt, stage0, bars);
   } else if (warp == 1) {
-    // ---------------- MMA issuer: one K-block into one accumulator
-    if (lane == 0) {
-      int64_t it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
-        for (int j = 0; j < g.kb; ++j, ++it) {
-          const int s = static_cast<int>(it % S), d = static_cast<int>(it & 1);
-          if (!mbar_wait_bounded(acc_empty(d), static_cast<uint32_t>((it >> 1) & 1) ^ 1u) ||
-              !mbar_wait_bounded(full_bar(s), static_cast<uint32_t>((it / S) & 1))) {
-            ok = false;
-            break;
-          }
+    // ---------------- MMA issuer (a pair's leader): one K-block into one accumulator.  The whole warp
+    // runs the loop, which keeps the descriptors in uniform registers; one lane issues
+    if (rank == 0) {
+      RingPos<S> r;
+      RingPos<NA> u;
+      bool ok = true, ready = false;
+      uint32_t last = 0;   // 1 | accumulator << 1 | parity << 8 of the last commit, 0: none
+      const uint64_t da0 = umma_smem_desc(a_tile(0), 1024, 2), db0 = umma_smem_desc(b_tile(0), 1024, 2);
+      for (int t = t0; ok && t < n_tiles; t += dt) {
+        for (int j = 0; j < g.kb; ++j) {
+          if (!__all_sync(0xFFFFFFFFu, ready))
+            ok = warp_wait2(full_bar(r.i), r.parity, acc_empty(u.i), u.parity ^ 1u, kMmaTries);
+          if (!ok) break;
           tc_fence_after();
+          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(r.i) * (Cfg::kStageBytes / 16));
+          RingPos<S> rn = r;
+          RingPos<NA> un = u;
+          rn.next();
+          un.next();
+          ready = mbar_test2(full_bar(rn.i), rn.parity, acc_empty(un.i), un.parity ^ 1u);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < Cfg::kBK / 32; ++kk)
-            umma_e4m3(tmem_base + d * BN, umma_smem_desc(a_tile(s) + kk * 32, 1024, 2),
-                      umma_smem_desc(b_tile(s) + kk * 32, 1024, 2), Cfg::kIdesc, kk != 0 ? 1u : 0u);
-          umma_commit(empty_bar(s));
-          umma_commit(acc_full(d));
+            for (int kk = 0; kk < Cfg::kBK / 32; ++kk)   // 32 bytes along K: 2 in the descriptors' units
+              gemm_fp8_mma<C>(tmem_base + u.i * BN, da0 + off + 2 * kk, db0 + off + 2 * kk, Cfg::kIdesc,
+                              kk != 0 ? 1u : 0u);
+            gemm_fp8_commit<C>(empty_bar(r.i));
+            gemm_fp8_commit<C>(acc_full(u.i));
+          }
+          __syncwarp();
+          last = 1u | static_cast<uint32_t>(u.i) << 1 | u.parity << 8;
+          r = rn;
+          u = un;
         }
       }
       // the last commits must have landed before TMEM is freed
-      if (it > 0) mbar_wait_bounded(acc_full(static_cast<int>((it - 1) & 1)), static_cast<uint32_t>(((it - 1) >> 1) & 1));
+      if (last) mbar_wait_bounded(acc_full((last >> 1) & 0x7F), last >> 8);
     }
-  } else {
-    // ---------------- adding warps: TMEM lane quarter warp % 4, column half (warp - 2) / 4
+  } else if (warp >= Cfg::kAddWarp0) {
+    // ---------------- adding warps: TMEM lane quarter warp % 4, column half (warp - 4) / 4
+    if constexpr (Cfg::kRegSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kRegsMany));
     const int q = warp & 3, half = (warp - Cfg::kAddWarp0) >> 2;
-    constexpr int NC = Cfg::kCols, CH = 16;
+    constexpr int NC = Cfg::kCols, CH = 8;
     pdl_wait();
-    int64_t it = 0;
+    RingPos<NA> u;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < n_tiles; t += gridDim.x) {
+    for (int t = t0; ok && t < n_tiles; t += dt) {
       const int tm = t % g.tiles_m, tn = t / g.tiles_m;
-      const int64_t row = static_cast<int64_t>(tm) * Cfg::kBM + 32 * q + lane;
+      const int64_t row = static_cast<int64_t>(tm) * Cfg::kBM + rank * 128 + 32 * q + lane;
       const int64_t col0 = static_cast<int64_t>(tn) * BN + half * NC;
       // rows and columns past the end use the last ones' scales; they are not stored
       const int64_t sa0 = (row < g.M ? row : g.M - 1) * g.kb;
       const int64_t sb0 = (col0 < g.N ? col0 : g.N - 1) / kFp8Block * g.kb;
-      // the scales of a block are loaded two blocks ahead
-      float s0 = load_scale<Cfg::kSf>(g.a_scales, sa0) * load_scale<Cfg::kSf>(g.b_scales, sb0);
-      const int j1 = g.kb > 1 ? 1 : 0;
-      float sa1 = load_scale<Cfg::kSf>(g.a_scales, sa0 + j1), sb1 = load_scale<Cfg::kSf>(g.b_scales, sb0 + j1);
+      // A block's scales are loaded two blocks ahead, into registers of their own by parity: a copy from
+      // one register to the next would wait for the load
+      float sa[2], sb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = i < g.kb ? i : 0;
+        sa[i] = load_scale<Cfg::kSf>(g.a_scales, sa0 + j);
+        sb[i] = load_scale<Cfg::kSf>(g.b_scales, sb0 + j);
+      }
       f32x2 acc[NC / 2];
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) acc[i] = 0ull;
 #pragma unroll 1
-      for (int j = 0; j < g.kb; ++j, ++it) {
-        const int d = static_cast<int>(it & 1);
-        const int j2 = j + 2 < g.kb ? j + 2 : g.kb - 1;
-        const float sa2 = load_scale<Cfg::kSf>(g.a_scales, sa0 + j2), sb2 = load_scale<Cfg::kSf>(g.b_scales, sb0 + j2);
-        const bool mine = mbar_wait_bounded(acc_full(d), static_cast<uint32_t>((it >> 1) & 1));
-        if (!__all_sync(0xFFFFFFFFu, mine)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const f32x2 s2 = f2_pack(s0, s0);
-        const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + d * BN + half * NC;
+      for (int jj = 0; ok && jj < g.kb; jj += 2) {
 #pragma unroll
-        for (int c = 0; c < NC / CH; ++c) {
-          uint32_t p[CH];
-          tmem_ld16_bits(src + c * CH, p);
-          tmem_wait(p);
-          if (c == NC / CH - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty(d));
-          }
+        for (int i = 0; i < 2; ++i) {
+          if (jj + i >= g.kb) break;
+          ok = warp_wait(acc_full(u.i), u.parity, 1);
+          if (!ok) break;
+          tc_fence_after();
+          const float s = sa[i] * sb[i];
+          const int j2 = jj + i + 2 < g.kb ? jj + i + 2 : g.kb - 1;
+          sa[i] = load_scale<Cfg::kSf>(g.a_scales, sa0 + j2);
+          sb[i] = load_scale<Cfg::kSf>(g.b_scales, sb0 + j2);
+          const f32x2 s2 = f2_pack(s, s);
+          const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + u.i * BN + half * NC;
 #pragma unroll
-          for (int i = 0; i < CH / 2; ++i) {
-            f32x2& x = acc[c * (CH / 2) + i];
-            x = f2_fma(f2_pack(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])), s2, x);
+          for (int c = 0; c < NC / CH; ++c) {
+            f32x2 p[CH / 2];
+            tmem_ld_pairs(src + c * CH, p);
+            if (c == NC / CH - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if constexpr (C == 2)
+                  mbar_arrive_cluster(cluster_map(acc_empty(u.i), 0));
+                else
+                  mbar_arrive(acc_empty(u.i));
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < CH / 2; ++k) acc[c * (CH / 2) + k] = f2_fma(p[k], s2, acc[c * (CH / 2) + k]);
           }
+          u.next();
         }
-        s0 = sa1 * sb1;
-        sa1 = sa2, sb1 = sb2;
       }
       if (ok && row < g.M) {
 #pragma unroll
@@ -297,11 +513,226 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       }
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (C == 2) cluster_sync_all();   // nothing of the pair's is in flight towards the other CTA
   if (warp == 1) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(Cfg::kTmemCols)
+    if constexpr (C == 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(Cfg::kTmemCols)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(Cfg::kTmemCols)
+                   : "memory");
+  }
+}
+
+// ---------------------------------------------------------------- many rows, scales in powers of two
+//
+// With E8M0 scales the tensor core applies them itself (kind::mxf8f6f4, a scale per row and 32
+// channels: a block's four MMAs name the same one), so a tile's whole sum stays in tensor memory and
+// nothing is added in registers.  A pair of CTAs takes 256 x 224 of D: two accumulators of 224 columns
+// leave room for the scales (12 columns, twice), and the epilogue of one tile runs under the MMAs of
+// the next.  The scales reach tensor memory without a copy instruction, which would wait its turn with
+// the MMAs: four warps, one per lane quarter, load four blocks' bytes of a row as one word and store it
+// (row r of the tile: lane r mod 32 of every quarter, column r / 32, byte j mod 4).
+template <int OT>
+struct GemmFp8MxConfig {
+  static constexpr int kCtas = 2, kBM = 256, kBN = 224, kBK = kFp8Block;
+  static constexpr int kOut = OT;
+  static constexpr int kARows = 128, kBRows = kBN / 2;      // a CTA's share of a stage
+  static constexpr int kABytes = kARows * kBK, kBBytes = kBRows * kBK;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static_assert(kStageBytes % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms");
+  static constexpr int kStages = (196 * 1024) / kStageBytes;
+  static constexpr int kBarOffset = kStages * kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kBarOffset + 256;
+  static constexpr int kSfCols = 4 + 8;                     // A's 128 rows, B's 224 in 32-row cells
+  static constexpr int kSfCol0 = 2 * kBN;
+  static constexpr int kTmemCols = 512;
+  static_assert(kSfCol0 + 2 * kSfCols <= kTmemCols);
+  static constexpr int kSfWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
+  static constexpr int kCols = kBN / 2;                     // columns per epilogue warp
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+  // as gemm_fp8_idesc, with E8M0 scales (bit 23)
+  static constexpr uint32_t kIdesc =
+      (1u << 23) | (static_cast<uint32_t>(kBN >> 3) << 17) | (static_cast<uint32_t>(kBM >> 4) << 24);
+};
+
+// The scale bytes of blocks j .. j + 3 of row `row` as one word; past the end of the row or of the rows
+// zeros, which meet no code but zeros.  vec: rows start on whole words.
+__device__ __forceinline__ uint32_t load_scale_word(const uint8_t* scales, int64_t row, int64_t rows, int j, int kb,
+                                                    bool vec) {
+  if (row >= rows) return 0u;
+  const uint8_t* p = scales + row * kb + j;
+  if (vec) return __ldg(reinterpret_cast<const uint32_t*>(p));
+  uint32_t w = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (j + i < kb) w |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
+  return w;
+}
+
+template <class Cfg>
+__global__ void __launch_bounds__(Cfg::kThreads, 1)
+    gemm_fp8_mx_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                       GemmFp8Args g) {
+  constexpr int S = Cfg::kStages, BN = Cfg::kBN, C = Cfg::kCtas;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem_base;
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const uint32_t stage0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bars = stage0 + Cfg::kBarOffset;
+  auto a_tile = [&](int s) { return stage0 + s * Cfg::kStageBytes; };
+  auto b_tile = [&](int s) { return stage0 + s * Cfg::kStageBytes + Cfg::kABytes; };
+  // what the MMA warp waits for is on the leader's barriers; what it commits arrives on both CTAs'
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
+  auto acc_full = [&](int d) { return bars + 8u * (2 * S + d); };
+  auto acc_empty = [&](int d) { return bars + 8u * (2 * S + 2 + d); };
+  auto sf_full = [&](int d) { return bars + 8u * (2 * S + 4 + d); };
+  auto sf_empty = [&](int d) { return bars + 8u * (2 * S + 6 + d); };
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int d = 0; d < 2; ++d) {
+      mbar_init(acc_full(d), 1);
+      mbar_init(acc_empty(d), C * Cfg::kEpiWarps);
+      mbar_init(sf_full(d), C * 4);
+      mbar_init(sf_empty(d), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem_base)),
+                 "r"(Cfg::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // the pair's barriers are set up
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem_base;
+  const int n_tiles = g.tiles_m * g.tiles_n;
+  const int t0 = static_cast<int>(blockIdx.x) / C, dt = static_cast<int>(gridDim.x) / C;
+
+  if (warp == 0) {
+    gemm_fp8_produce<Cfg>(g, amap, bmap, rank, t0, dt, stage0, bars);
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (the leader)
+    if (rank == 0) {
+      RingPos<S> r;
+      RingPos<2> u, f;
+      bool ok = true, ready = false;
+      uint32_t last = 0;   // 1 | accumulator << 1 | parity << 8 of the last commit, 0: none
+      const uint64_t da0 = umma_smem_desc(a_tile(0), 1024, 2), db0 = umma_smem_desc(b_tile(0), 1024, 2);
+      for (int t = t0; ok && t < n_tiles; t += dt) {
+        ok = warp_wait(acc_empty(u.i), u.parity ^ 1u, kMmaTries);
+        for (int j = 0; ok && j < g.kb; ++j) {
+          if ((j & 3) == 0) ok = warp_wait(sf_full(f.i), f.parity, kMmaTries);
+          if (!__all_sync(0xFFFFFFFFu, ready)) ok = ok && warp_wait(full_bar(r.i), r.parity, kMmaTries);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(r.i) * (Cfg::kStageBytes / 16));
+          RingPos<S> rn = r;
+          rn.next();
+          ready = mbar_test(full_bar(rn.i), rn.parity);
+          const uint32_t id = static_cast<uint32_t>(j & 3);   // the block's byte in the scales' cells
+          const uint32_t idesc = Cfg::kIdesc | (id << 4) | (id << 29);
+          const uint32_t sfa = (tmem_base + Cfg::kSfCol0 + f.i * Cfg::kSfCols) | (id << 30), sfb = sfa + 4;
+          const bool group_end = (j & 3) == 3 || j == g.kb - 1;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < Cfg::kBK / 32; ++kk)
+              umma_e4m3_scaled(tmem_base + u.i * BN, da0 + off + 2 * kk, db0 + off + 2 * kk, idesc, sfa, sfb,
+                               (j | kk) != 0 ? 1u : 0u);
+            gemm_fp8_commit<C>(empty_bar(r.i));
+            if (group_end) gemm_fp8_commit<C>(sf_empty(f.i));
+            if (j == g.kb - 1) gemm_fp8_commit<C>(acc_full(u.i));
+          }
+          __syncwarp();
+          if (group_end) f.next();
+          r = rn;
+        }
+        if (ok) last = 1u | static_cast<uint32_t>(u.i) << 1 | u.parity << 8;
+        u.next();
+      }
+      // the last commits must have landed before TMEM is freed
+      if (last) mbar_wait_bounded(acc_full((last >> 1) & 1u), last >> 8);
+    }
+  } else if (warp >= Cfg::kEpiWarp0) {
+    // ---------------- epilogue: lane quarter warp % 4, column half (warp - 8) / 4
+    const int q = warp & 3, half = (warp - Cfg::kEpiWarp0) >> 2;
+    constexpr int NC = Cfg::kCols;
+    pdl_wait();   // D may still be read by an earlier kernel
+    RingPos<2> u;
+    for (int t = t0; t < n_tiles; t += dt, u.next()) {
+      const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+      const int64_t row = static_cast<int64_t>(tm) * Cfg::kBM + rank * 128 + 32 * q + lane;
+      const int64_t col0 = static_cast<int64_t>(tn) * BN + half * NC;
+      if (!warp_wait(acc_full(u.i), u.parity, 0)) break;
+      tc_fence_after();
+      const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + u.i * BN + half * NC;
+#pragma unroll 1
+      for (int c = 0; c < NC / 16; ++c) {
+        f32x2 p[8];
+        tmem_ld_pairs(src + 16 * c, p);
+        if (row < g.M && col0 + 16 * c < g.N) store_row16<Cfg::kOut>(g, row, col0 + 16 * c, p);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_map(acc_empty(u.i), 0));
+    }
+  } else if (warp >= Cfg::kSfWarp0) {
+    // ---------------- scales into tensor memory: lane quarter warp % 4, all quarters alike
+    const int q = warp & 3;
+    const auto* as = static_cast<const uint8_t*>(g.a_scales);
+    const auto* bs = static_cast<const uint8_t*>(g.b_scales);
+    const int64_t b_rows = (g.N + kFp8Block - 1) / kFp8Block;
+    pdl_wait();
+    RingPos<2> f;
+    bool ok = true;
+    for (int t = t0; ok && t < n_tiles; t += dt) {
+      const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+      const int64_t ra = static_cast<int64_t>(tm) * Cfg::kBM + rank * 128 + lane;
+      const int64_t rb = static_cast<int64_t>(tn) * BN + lane;
+      for (int j = 0; j < g.kb; j += 4, f.next()) {
+        uint32_t wa[4], wb[8];   // the loads run while the buffer is waited for
+#pragma unroll
+        for (int i = 0; i < 4; ++i) wa[i] = load_scale_word(as, ra + 32 * i, g.M, j, g.kb, g.sf_vec);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wb[i] = i < BN / 32 ? load_scale_word(bs, (rb + 32 * i) / kFp8Block, b_rows, j, g.kb, g.sf_vec) : 0u;
+        ok = warp_wait(sf_empty(f.i), f.parity ^ 1u, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dst = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + Cfg::kSfCol0 + f.i * Cfg::kSfCols;
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(wa[0]), "r"(wa[1]),
+                     "r"(wa[2]), "r"(wa[3])
+                     : "memory");
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(dst + 4), "r"(wb[0]),
+                     "r"(wb[1]), "r"(wb[2]), "r"(wb[3]), "r"(wb[4]), "r"(wb[5]), "r"(wb[6]), "r"(wb[7])
+                     : "memory");
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_map(sf_full(f.i), 0));
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();   // nothing of the pair's is in flight towards the other CTA
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(Cfg::kTmemCols)
                  : "memory");
   }
 }
@@ -310,69 +741,80 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 //
 // For decode batches the product is a stream of B: here B is the MMA's row operand (tiles of 128 of
 // its rows, one scale per tile and block) and BT rows of A are its columns, so no MMA row is idle.
-// The blocks of K are split over a cluster of `split` CTAs, so that enough loads are in flight on
-// all SMs; each CTA leaves its sums in shared memory and takes its share of the tokens from all of
-// them, in the order of their ranks (no atomics, no workspace).
+// One CTA to an SM and one tile to a CTA; where there are fewer tiles than SMs, the blocks of K are
+// split over a cluster.  A CTA's sums then go to the CTA of the cluster that owns their token (pushed
+// into its shared memory), which adds them in the order of their ranks: no atomics, no workspace.
 template <int BT_, int OT, int SF>
 struct GemmFp8FewConfig {
   static constexpr int kBT = BT_, kBK = kFp8Block;
   static constexpr int kOut = OT, kSf = SF;
+  static constexpr int kMaxSplit = 8;                                // portable cluster size
   static constexpr int kWBytes = 128 * kBK, kXBytes = kBT * kBK;
   static constexpr int kStageBytes = kWBytes + kXBytes;
-  // two CTAs on an SM: 228 KB less 1 KB of system use each
-  static constexpr int kStages = (110 * 1024) / kStageBytes;
-  static constexpr int kBarOffset = kStages * kStageBytes;
-  static constexpr int kSmemBytes = 1024 + kBarOffset + 256;
-  static constexpr int kTmemCols = 2 * kBT < 32 ? 32 : 2 * kBT;
-  static constexpr int kAddWarp0 = 2, kAddWarps = 4;
+  static constexpr int kHalves = kBT > 32 ? 2 : 1;                   // adding warps per TMEM lane quarter
+  static constexpr int kTok = kBT / kHalves;                         // tokens per adding warp
+  static constexpr int kAddWarp0 = 4, kAddWarps = 4 * kHalves;
   static constexpr int kThreads = 32 * (kAddWarp0 + kAddWarps);
+  static constexpr int kSumBytes = kBT * 128 * 4;                    // one tile's sums
+  static constexpr int kMultBytes = kAddWarps * 2 * kTok * 4;        // per adding warp: two blocks' multipliers
+  static constexpr int kStages = (222 * 1024 - kSumBytes - kMultBytes) / kStageBytes;
+  static constexpr int kBarOffset = kStages * kStageBytes;
+  static constexpr int kMultOffset = kBarOffset + 512;
+  static constexpr int kSumOffset = kMultOffset + kMultBytes;
+  static constexpr int kSmemBytes = 1024 + kSumOffset + kSumBytes;
+  static constexpr int kAccs = 4;
+  static constexpr int kTmemCols = kAccs * kBT;
   static constexpr uint32_t kIdesc = gemm_fp8_idesc(128, kBT);
   static_assert(kStageBytes % 1024 == 0, "stages stay 1024-byte aligned (128-byte swizzle atoms)");
-  static_assert(kBT * 128 * 4 <= kBarOffset, "a CTA's sums fit in the ring");
+  static_assert(8 * (2 * kStages + 2 * kAccs) <= 512 && kSumOffset % 16 == 0 && kSmemBytes <= 227 * 1024);
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// One thread's sums to the CTAs that own their tokens (token i: CTA i / (BT / SPLIT)), as
+// sums[rank][token of the owner][row nl].  SPLIT is a constant so that nothing is divided: with a
+// variable one the 64 stores of a thread took 6.7 us.
+template <int SPLIT, int BT, int TOK>
+__device__ __forceinline__ void few_push(const f32x2 (&acc)[TOK / 2], uint32_t sums, int rank, int tok0, int nl) {
+  constexpr int OWN = BT / SPLIT, PER = OWN < TOK ? OWN : TOK;   // tokens of one owner in this thread
+#pragma unroll
+  for (int o = 0; o < TOK / PER; ++o) {
+    const int tok = tok0 + o * PER, owner = tok / OWN;
+    const uint32_t local = sums + 4u * ((rank * OWN + (tok - owner * OWN)) * 128 + nl);
+    const uint32_t to = SPLIT > 1 ? cluster_map(local, owner) : local;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      float v[2];
+      f2_unpack(acc[(o * PER + i) / 2], v[0], v[1]);
+      if constexpr (SPLIT > 1)
+        st_cluster_f32(to + 512u * i, v[i & 1]);
+      else
+        sts32(to + 512u * i, __float_as_uint(v[i & 1]));
+    }
+  }
 }
 
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::kThreads, 2)
+__global__ void __launch_bounds__(Cfg::kThreads, 1)
     gemm_fp8_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                         GemmFp8Args g, int split) {
-  constexpr int S = Cfg::kStages, BT = Cfg::kBT;
+  constexpr int S = Cfg::kStages, BT = Cfg::kBT, NA = Cfg::kAccs, TOK = Cfg::kTok;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   pdl_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t stage0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t bars = stage0 + Cfg::kBarOffset;
+  const uint32_t bars = stage0 + Cfg::kBarOffset, sums = stage0 + Cfg::kSumOffset;
   auto w_tile = [&](int s) { return stage0 + s * Cfg::kStageBytes; };
   auto x_tile = [&](int s) { return stage0 + s * Cfg::kStageBytes + Cfg::kWBytes; };
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (S + s); };
   auto acc_full = [&](int d) { return bars + 8u * (2 * S + d); };
-  auto acc_empty = [&](int d) { return bars + 8u * (2 * S + 2 + d); };
+  auto acc_empty = [&](int d) { return bars + 8u * (2 * S + NA + d); };
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int d = 0; d < 2; ++d) {
+    for (int d = 0; d < NA; ++d) {
       mbar_init(acc_full(d), 1);
       mbar_init(acc_empty(d), Cfg::kAddWarps);
     }
@@ -386,6 +828,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
+  // the cluster's CTAs are running, so that their shared memory can be written; awaited below
+  if (split > 1) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -393,122 +837,150 @@ __global__ void __launch_bounds__(Cfg::kThreads, 2)
   const int tn = t % g.tiles_n, tm = t / g.tiles_n;
   const int j0 = static_cast<int>(static_cast<int64_t>(g.kb) * rank / split);
   const int j1 = static_cast<int>(static_cast<int64_t>(g.kb) * (rank + 1) / split);
-  const int nj = j1 - j0;
+  const int64_t m0 = static_cast<int64_t>(tm) * BT, n0 = static_cast<int64_t>(tn) * 128;
+  const int own = BT / split;   // tokens whose sums this CTA takes: rank * own ...
 
   if (warp == 0) {
     if (lane == 0) {
       pdl_wait();
-      int it = 0;
-      for (; it < nj; ++it) {
-        const int s = it % S;
-        if (!mbar_wait_bounded(empty_bar(s), static_cast<uint32_t>((it / S) & 1) ^ 1u)) break;
-        mbar_arrive_expect_tx(full_bar(s), Cfg::kStageBytes);
-        tma_load_2d(w_tile(s), &wmap, (j0 + it) * Cfg::kBK, tn * 128, full_bar(s));
-        tma_load_2d(x_tile(s), &xmap, (j0 + it) * Cfg::kBK, tm * BT, full_bar(s));
+      RingPos<S> r;
+      int filled = 0;
+      for (int j = j0; j < j1; ++j, r.next()) {
+        if (!mbar_test(empty_bar(r.i), r.parity ^ 1u) && !mbar_wait_bounded(empty_bar(r.i), r.parity ^ 1u)) break;
+        mbar_arrive_expect_tx(full_bar(r.i), Cfg::kStageBytes);
+        tma_load_2d(w_tile(r.i), &wmap, j * Cfg::kBK, tn * 128, full_bar(r.i));
+        tma_load_2d(x_tile(r.i), &xmap, j * Cfg::kBK, tm * BT, full_bar(r.i));
+        filled = filled < S ? filled + 1 : S;
       }
-      for (int j = (it > S ? it - S : 0); j < it; ++j) mbar_wait_bounded(full_bar(j % S), static_cast<uint32_t>((j / S) & 1));
+      // every issued copy lands before the CTA leaves
+      if (filled < S) r = RingPos<S>{};
+      for (int j = 0; j < filled; ++j, r.next()) mbar_wait_bounded(full_bar(r.i), filled < S ? 0u : r.parity ^ 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int it = 0;
-      for (; it < nj; ++it) {
-        const int s = it % S, d = it & 1;
-        if (!mbar_wait_bounded(acc_empty(d), static_cast<uint32_t>((it >> 1) & 1) ^ 1u) ||
-            !mbar_wait_bounded(full_bar(s), static_cast<uint32_t>((it / S) & 1)))
-          break;
-        tc_fence_after();
+    RingPos<S> r;
+    RingPos<NA> u;
+    bool ready = false;
+    uint32_t last = 0;   // 1 | accumulator << 1 | parity << 8 of the last commit, 0: none
+    const uint64_t dw0 = umma_smem_desc(w_tile(0), 1024, 2), dx0 = umma_smem_desc(x_tile(0), 1024, 2);
+    for (int j = j0; j < j1; ++j) {
+      if (!__all_sync(0xFFFFFFFFu, ready) &&
+          !warp_wait2(full_bar(r.i), r.parity, acc_empty(u.i), u.parity ^ 1u, kMmaTries))
+        break;
+      tc_fence_after();
+      const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(r.i) * (Cfg::kStageBytes / 16));
+      RingPos<S> rn = r;
+      RingPos<NA> un = u;
+      rn.next();
+      un.next();
+      ready = mbar_test2(full_bar(rn.i), rn.parity, acc_empty(un.i), un.parity ^ 1u);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < Cfg::kBK / 32; ++kk)
-          umma_e4m3(tmem_base + d * BT, umma_smem_desc(w_tile(s) + kk * 32, 1024, 2),
-                    umma_smem_desc(x_tile(s) + kk * 32, 1024, 2), Cfg::kIdesc, kk != 0 ? 1u : 0u);
-        umma_commit(empty_bar(s));
-        umma_commit(acc_full(d));
+          umma_e4m3(tmem_base + u.i * BT, dw0 + off + 2 * kk, dx0 + off + 2 * kk, Cfg::kIdesc, kk != 0 ? 1u : 0u);
+        umma_commit(empty_bar(r.i));
+        umma_commit(acc_full(u.i));
       }
-      if (it > 0) mbar_wait_bounded(acc_full((it - 1) & 1), static_cast<uint32_t>(((it - 1) >> 1) & 1));
+      __syncwarp();
+      last = 1u | static_cast<uint32_t>(u.i) << 1 | u.parity << 8;
+      r = rn;
+      u = un;
     }
-  } else {
-    // lane quarter warp % 4: this thread holds B's row n and the tile's BT tokens
-    const int q = warp & 3;
-    const int nl = 32 * q + lane;
-    const int64_t n = static_cast<int64_t>(tn) * 128 + nl;
-    const int64_t m0 = static_cast<int64_t>(tm) * BT;
-    constexpr int TL = (BT + 31) / 32;   // tokens whose scales a lane loads
+    if (last) mbar_wait_bounded(acc_full((last >> 1) & 0x7F), last >> 8);
+  } else if (warp >= Cfg::kAddWarp0) {
+    // lane quarter warp % 4: this thread holds B's row n0 + nl and TOK of the tile's tokens, from `tok0` on
+    const int q = warp & 3, nl = 32 * q + lane;
+    const int tok0 = ((warp - Cfg::kAddWarp0) >> 2) * TOK;
+    constexpr int TL = (TOK + 31) / 32;   // tokens whose multipliers a lane works out
+    const uint32_t mult = stage0 + Cfg::kMultOffset + (warp - Cfg::kAddWarp0) * (2 * TOK * 4);
     pdl_wait();
     const int64_t sb0 = static_cast<int64_t>(tn) * g.kb;
     int64_t sa0[TL];
 #pragma unroll
     for (int i = 0; i < TL; ++i) {
-      const int64_t m = m0 + i * 32 + lane;
+      const int64_t m = m0 + tok0 + i * 32 + lane;
       sa0[i] = (m < g.M ? m : g.M - 1) * g.kb;
     }
-    // lane l loads the product of the scales of token 32 i + l, two blocks ahead
-    auto scales = [&](int j, float (&v)[TL]) {
+    // lane l takes tokens 32 i + l: their scales of a block and the tile's, loaded two blocks ahead (into
+    // registers of their own by parity, as above), multiplied, and passed to the warp's other lanes
+    // through shared memory
+    auto scales = [&](int j, float (&v)[TL], float& sb) {
       const int jj = j < j1 ? j : (j1 > 0 ? j1 - 1 : 0);
-      const float sb = load_scale<Cfg::kSf>(g.b_scales, sb0 + jj);
+      sb = load_scale<Cfg::kSf>(g.b_scales, sb0 + jj);
 #pragma unroll
-      for (int i = 0; i < TL; ++i) v[i] = load_scale<Cfg::kSf>(g.a_scales, sa0[i] + jj) * sb;
+      for (int i = 0; i < TL; ++i) v[i] = load_scale<Cfg::kSf>(g.a_scales, sa0[i] + jj);
     };
-    float s0[TL], s1[TL], s2[TL];
-    scales(j0, s0);
-    scales(j0 + 1, s1);
-    float acc[BT];
+    auto put = [&](int slot, const float (&v)[TL], float sb) {
 #pragma unroll
-    for (int i = 0; i < BT; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < TL; ++i)
+        if (32 * i + lane < TOK) sts32(mult + 4u * (slot * TOK + 32 * i + lane), __float_as_uint(v[i] * sb));
+    };
+    float sa[2][TL], sb[2];
+    scales(j0, sa[0], sb[0]);
+    scales(j0 + 1, sa[1], sb[1]);
+    f32x2 acc[TOK / 2];
+#pragma unroll
+    for (int i = 0; i < TOK / 2; ++i) acc[i] = 0ull;
+    RingPos<NA> u;
+    bool ok = true;
 #pragma unroll 1
-    for (int it = 0; it < nj; ++it) {
-      const int d = it & 1;
-      scales(j0 + it + 2, s2);
-      const bool mine = mbar_wait_bounded(acc_full(d), static_cast<uint32_t>((it >> 1) & 1));
-      if (!__all_sync(0xFFFFFFFFu, mine)) break;
-      tc_fence_after();
-      const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + d * BT;
+    for (int jj = j0; ok && jj < j1; jj += 2) {
 #pragma unroll
-      for (int c = 0; c < BT / 16; ++c) {
-        uint32_t p[16];
-        tmem_ld16_bits(src + c * 16, p);
-        tmem_wait(p);
-        if (c == BT / 16 - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(acc_empty(d));
-        }
+      for (int i = 0; i < 2; ++i) {
+        if (jj + i >= j1) break;
+        put(i, sa[i], sb[i]);
+        scales(jj + i + 2, sa[i], sb[i]);
+        ok = warp_wait(acc_full(u.i), u.parity, 1);
+        if (!ok) break;
+        __syncwarp();   // the lanes' multipliers
+        tc_fence_after();
+        const uint32_t src = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + u.i * BT + tok0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int tok = c * 16 + i;
-          acc[tok] = fmaf(__uint_as_float(p[i]), __shfl_sync(0xFFFFFFFFu, s0[tok / 32], tok % 32), acc[tok]);
+        for (int c = 0; c < TOK / 16; ++c) {
+          f32x2 p[8], m[8];
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) lds_pairs(mult + 4u * (i * TOK + 16 * c + 2 * k), m[k], m[k + 1]);
+          tmem_ld_pairs(src + c * 16, p);
+          if (c == TOK / 16 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty(u.i));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[8 * c + k] = f2_fma(p[k], m[k], acc[8 * c + k]);
         }
+        u.next();
       }
-#pragma unroll
-      for (int i = 0; i < TL; ++i) s0[i] = s1[i], s1[i] = s2[i];
     }
-    if (split == 1) {
-      if (n < g.N) {
-#pragma unroll
-        for (int i = 0; i < BT; ++i)
-          if (m0 + i < g.M) store_one<Cfg::kOut>(g.d, (m0 + i) * g.N + n, acc[i]);
-      }
-    } else {
-      // every copy of the ring has landed and been read (the last block's MMAs are complete)
-#pragma unroll
-      for (int i = 0; i < BT; ++i) sts32(stage0 + 4u * (i * 128 + nl), __float_as_uint(acc[i]));
+    if (split > 1) cluster_wait();
+    switch (split) {
+      case 8: few_push<8, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      case 4: few_push<4, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      case 2: few_push<2, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      default: few_push<1, BT, TOK>(acc, sums, rank, tok0, nl); break;
     }
   }
+  __syncwarp();
   if (split > 1) {
-    __syncwarp();
+    if (warp < Cfg::kAddWarp0) cluster_wait();
     cluster_sync_all();
-    if (warp >= Cfg::kAddWarp0) {
-      const int nl = 32 * (warp & 3) + lane;
-      const int64_t n = static_cast<int64_t>(tn) * 128 + nl;
-      for (int i = rank; i < BT; i += split) {
-        const int64_t m = static_cast<int64_t>(tm) * BT + i;
-        if (m >= g.M) break;
-        float v = 0.0f;
-        for (int r = 0; r < split; ++r) v += ld_cluster_f32(cluster_map(stage0 + 4u * (i * 128 + nl), r));
-        if (n < g.N) store_one<Cfg::kOut>(g.d, m * g.N + n, v);
-      }
+  } else {
+    __syncthreads();
+  }
+  // eight neighbouring columns of one token a thread: 16-byte reads and stores
+  for (int c = tid; c < own * 16; c += Cfg::kThreads) {
+    const int64_t m = m0 + rank * own + c / 16, n = n0 + 8 * (c % 16);
+    if (m >= g.M || n >= g.N) continue;
+    f32x2 v[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+    for (int r = 0; r < split; ++r) {
+      f32x2 a[4];
+      const uint32_t at = sums + 4u * ((r * own + c / 16) * 128 + 8 * (c % 16));
+      lds_pairs(at, a[0], a[1]);
+      lds_pairs(at + 16, a[2], a[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_add(v[i], a[i]);
     }
-    __syncwarp();
-    cluster_sync_all();   // no CTA leaves while another reads its sums
+    store_row8<Cfg::kOut>(g, m, n, v);
   }
   tc_fence_before();
   __syncthreads();

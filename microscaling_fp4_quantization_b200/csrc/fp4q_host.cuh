@@ -50,19 +50,21 @@ constexpr int kLastErrorBytes = 512;
 struct KernelInfo {
   int ctas_per_sm = 0;
   int sm_count = 0;
+  int max_clusters = 0;   // clusters of the size asked for that are resident at once (0: none asked for)
 };
 // Occupancy is computed for smem_bytes, the dynamic shared memory of the launch; the kernel
 // may be launched with up to max_smem_bytes (when larger), which every call for one kernel
 // passes alike.  Results are cached per (kernel, context, smem_bytes, threads).
 // carveout: the share of the unified L1 / shared storage kept as shared memory, in percent (-1:
-// the driver's choice, for kernels that stream through L1).
+// the driver's choice, for kernels that stream through L1).  cluster: CTAs per cluster of the launch.
 fp4q_status kernel_info_impl(const void* kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes,
-                             int carveout = 100);
+                             int carveout = 100, int cluster = 1);
 
 template <class K>
 fp4q_status kernel_info(K kernel, int smem_bytes, int threads, KernelInfo* out, int max_smem_bytes = 0,
-                        int carveout = 100) {
-  return kernel_info_impl(reinterpret_cast<const void*>(kernel), smem_bytes, threads, out, max_smem_bytes, carveout);
+                        int carveout = 100, int cluster = 1) {
+  return kernel_info_impl(reinterpret_cast<const void*>(kernel), smem_bytes, threads, out, max_smem_bytes, carveout,
+                          cluster);
 }
 
 // The butterfly kernels (rotate + quantize, error pass, amax) may stage a sign mask of up to
@@ -77,6 +79,26 @@ fp4q_status butterfly_kernel_info(K kernel, KernelInfo* out, int smem_words = 0)
 // Launch with programmatic stream serialization, so the kernel's start overlaps the tail of
 // the previous kernel on the stream (the kernels wait on the dependency before touching
 // global memory).
+// launch_pdl_cluster: in clusters of that many CTAs along x.
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                               cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                        Args&&... args) {

@@ -29,76 +29,135 @@ fp4q_status codes_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t
   return FP4Q_OK;
 }
 
-template <class Cfg>
-fp4q_status launch_many(const void* a_codes, const void* b_codes, GemmFp8Args g, int64_t K, cudaStream_t stream) {
+struct Problem {
+  const void *a_codes, *b_codes;
+  GemmFp8Args g;
+  int64_t K;
+  cudaStream_t stream;
+};
+
+// The many-row kernels: persistent clusters (pairs) or CTAs, as many as are resident at once.
+template <class Cfg, class Kernel>
+fp4q_status launch_many(Kernel kernel, Problem p) {
   CUtensorMap amap, bmap;
-  fp4q_status st = codes_map(&amap, a_codes, g.M, K, Cfg::kBM);
-  if (st == FP4Q_OK) st = codes_map(&bmap, b_codes, g.N, K, Cfg::kBN);
+  fp4q_status st = codes_map(&amap, p.a_codes, p.g.M, p.K, Cfg::kARows);
+  if (st == FP4Q_OK) st = codes_map(&bmap, p.b_codes, p.g.N, p.K, Cfg::kBRows);
   if (st != FP4Q_OK) return st;
-  g.tiles_m = static_cast<int>((g.M + Cfg::kBM - 1) / Cfg::kBM);
-  g.tiles_n = static_cast<int>((g.N + Cfg::kBN - 1) / Cfg::kBN);
-  auto kernel = gemm_fp8_kernel<Cfg>;
+  p.g.tiles_m = static_cast<int>((p.g.M + Cfg::kBM - 1) / Cfg::kBM);
+  p.g.tiles_n = static_cast<int>((p.g.N + Cfg::kBN - 1) / Cfg::kBN);
   KernelInfo ki;
-  st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki);
+  st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki, 0, 100, Cfg::kCtas);
   if (st != FP4Q_OK) return st;
-  int64_t ctas = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
-  if (ctas > ki.sm_count) ctas = ki.sm_count;
-  cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
-                             amap, bmap, g);
+  int64_t n = static_cast<int64_t>(p.g.tiles_m) * p.g.tiles_n;
+  const int64_t resident = Cfg::kCtas > 1 ? ki.max_clusters : ki.sm_count;
+  if (n > resident) n = resident;
+  cudaError_t e = launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(n * Cfg::kCtas)), dim3(Cfg::kThreads),
+                                     Cfg::kSmemBytes, Cfg::kCtas, p.stream, amap, bmap, p.g);
   if (e != cudaSuccess) return cuda_fail(e, "gemm_fp8 launch");
   return FP4Q_OK;
 }
 
+// The warps that hand their registers over can do so only if the launch holds them.
+template <class Cfg, class Kernel>
+fp4q_status check_registers(Kernel kernel) {
+  if constexpr (Cfg::kRegSplit) {
+    static const int regs = [&] {
+      cudaFuncAttributes fa = {};
+      return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess ? fa.numRegs : 0;
+    }();
+    if (regs < Cfg::kRegsLaunch) {
+      std::snprintf(last_error_buffer(), kLastErrorBytes, "gemm_fp8: built with %d registers a thread, not %d", regs,
+                    Cfg::kRegsLaunch);
+      return FP4Q_ERR_UNSUPPORTED;
+    }
+  }
+  return FP4Q_OK;
+}
+
+template <int CTAS, int BN, int OT, int SF>
+fp4q_status launch_add(const Problem& p) {
+  using Cfg = GemmFp8Config<CTAS, BN, OT, SF>;
+  fp4q_status st = check_registers<Cfg>(gemm_fp8_kernel<Cfg>);
+  return st == FP4Q_OK ? launch_many<Cfg>(gemm_fp8_kernel<Cfg>, p) : st;
+}
+
 template <class Cfg>
-fp4q_status launch_few(const void* a_codes, const void* b_codes, GemmFp8Args g, int64_t K, cudaStream_t stream) {
+fp4q_status launch_few(Problem p, int split) {
   CUtensorMap wmap, xmap;
-  fp4q_status st = codes_map(&wmap, b_codes, g.N, K, 128);
-  if (st == FP4Q_OK) st = codes_map(&xmap, a_codes, g.M, K, Cfg::kBT);
+  fp4q_status st = codes_map(&wmap, p.b_codes, p.g.N, p.K, 128);
+  if (st == FP4Q_OK) st = codes_map(&xmap, p.a_codes, p.g.M, p.K, Cfg::kBT);
   if (st != FP4Q_OK) return st;
-  g.tiles_m = static_cast<int>((g.M + Cfg::kBT - 1) / Cfg::kBT);
-  g.tiles_n = static_cast<int>((g.N + 127) / 128);
+  p.g.tiles_m = static_cast<int>((p.g.M + Cfg::kBT - 1) / Cfg::kBT);
+  p.g.tiles_n = static_cast<int>((p.g.N + 127) / 128);
   auto kernel = gemm_fp8_few_kernel<Cfg>;
+  const int64_t tiles = static_cast<int64_t>(p.g.tiles_m) * p.g.tiles_n;
   KernelInfo ki;
-  st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki);
+  st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki, 0, 100, split);
   if (st != FP4Q_OK) return st;
-  // split K over a cluster as long as all CTAs stay resident together (two on an SM)
-  const int64_t tiles = static_cast<int64_t>(g.tiles_m) * g.tiles_n;
-  int split = 1;
-  while (split < 8 && 2 * split <= g.kb && tiles * 2 * split <= 2 * static_cast<int64_t>(ki.sm_count)) split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, wmap, xmap, g, split);
+  // a cluster takes `split` SMs of one GPC: where they do not all fit at once, split less
+  while (split > 1 && tiles > ki.max_clusters) {
+    split /= 2;
+    st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki, 0, 100, split);
+    if (st != FP4Q_OK) return st;
+  }
+  cudaError_t e = launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(tiles * split)), dim3(Cfg::kThreads),
+                                     Cfg::kSmemBytes, split, p.stream, wmap, xmap, p.g, split);
   if (e != cudaSuccess) return cuda_fail(e, "gemm_fp8 launch");
   return FP4Q_OK;
+}
+
+// Which kernel: the one whose time, as a start and a number of blocks of K worked off one after another,
+// comes out least.  Starts and times per block (in units of 10 ns) are those measured on 148 SMs, with
+// operands in L2: see the table in the design notes for both sides of each choice.
+struct Variant {
+  int tile_m, tile_n;   // of D
+  int ctas;             // per tile
+  int start, block;
+};
+constexpr Variant kFew16{16, 128, 1, 330, 22}, kFew32{32, 128, 1, 330, 26}, kFew64{64, 128, 1, 330, 30},
+    kOne128{128, 128, 1, 450, 31}, kPair128{256, 128, 2, 450, 30}, kPair256{256, 256, 2, 450, 52},
+    kPairMx{256, 224, 2, 450, 31};
+
+struct Estimate {
+  int64_t time;
+  int split;
+};
+Estimate estimate(const Variant& v, const GemmFp8Args& g, int sms, bool may_split) {
+  const int64_t tiles = ((g.M + v.tile_m - 1) / v.tile_m) * ((g.N + v.tile_n - 1) / v.tile_n);
+  const int64_t at_once = sms / v.ctas;
+  const int64_t rounds = (tiles + at_once - 1) / at_once;
+  int split = 1;
+  while (may_split && split < 8 && tiles * 2 * split <= at_once && g.kb >= 4 * split) split *= 2;
+  return {v.start + (split > 1 ? 40 : 0) + rounds * ((g.kb + split - 1) / split) * v.block, split};
 }
 
 template <int OT, int SF>
-fp4q_status dispatch(const void* a_codes, const void* b_codes, const GemmFp8Args& g, int64_t K, cudaStream_t stream) {
-  if (g.M <= 16) return launch_few<GemmFp8FewConfig<16, OT, SF>>(a_codes, b_codes, g, K, stream);
-  if (g.M <= 32) return launch_few<GemmFp8FewConfig<32, OT, SF>>(a_codes, b_codes, g, K, stream);
-  if (g.M <= 64) return launch_few<GemmFp8FewConfig<64, OT, SF>>(a_codes, b_codes, g, K, stream);
-  const int64_t tiles256 = (g.M + 127) / 128 * ((g.N + 255) / 256);
-  if (tiles256 < 148) return launch_many<GemmFp8Config<128, OT, SF>>(a_codes, b_codes, g, K, stream);
-  return launch_many<GemmFp8Config<256, OT, SF>>(a_codes, b_codes, g, K, stream);
+fp4q_status dispatch(const Problem& p) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  const GemmFp8Args& g = p.g;
+  const Estimate few = estimate(g.M <= 16 ? kFew16 : g.M <= 32 ? kFew32 : kFew64, g, sms, true);
+  const int64_t one = estimate(kOne128, g, sms, false).time, pair = estimate(kPair128, g, sms, false).time;
+  const int64_t wide = estimate(SF == kSfE8m0 ? kPairMx : kPair256, g, sms, false).time;
+  if (few.time <= one && few.time <= pair && few.time <= wide) {
+    if (g.M <= 16) return launch_few<GemmFp8FewConfig<16, OT, SF>>(p, few.split);
+    if (g.M <= 32) return launch_few<GemmFp8FewConfig<32, OT, SF>>(p, few.split);
+    return launch_few<GemmFp8FewConfig<64, OT, SF>>(p, few.split);
+  }
+  if (wide <= one && wide <= pair) {
+    if constexpr (SF == kSfE8m0)
+      return launch_many<GemmFp8MxConfig<OT>>(gemm_fp8_mx_kernel<GemmFp8MxConfig<OT>>, p);
+    else
+      return launch_add<2, 256, OT, SF>(p);
+  }
+  return pair < one ? launch_add<2, 128, OT, SF>(p) : launch_add<1, 128, OT, SF>(p);
 }
 
 template <int OT>
-fp4q_status dispatch_sf(int scale_format, const void* a_codes, const void* b_codes, const GemmFp8Args& g, int64_t K,
-                        cudaStream_t stream) {
-  return scale_format == FP4Q_FP8_SCALE_F32 ? dispatch<OT, kSfF32>(a_codes, b_codes, g, K, stream)
-                                            : dispatch<OT, kSfE8m0>(a_codes, b_codes, g, K, stream);
+fp4q_status dispatch_sf(int scale_format, const Problem& p) {
+  return scale_format == FP4Q_FP8_SCALE_F32 ? dispatch<OT, kSfF32>(p) : dispatch<OT, kSfE8m0>(p);
 }
 
 }  // namespace
@@ -116,10 +175,13 @@ fp4q_status launch_gemm_fp8(int scale_format, int out_dtype, const void* a_codes
   const int64_t esize = out_dtype == FP4Q_DTYPE_F32 ? 4 : 2;
   const uintptr_t at = reinterpret_cast<uintptr_t>(d);
   g.vec = (at % 32 == 0 && N * esize % 32 == 0) ? 2 : (N * esize % 16 == 0) ? 1 : 0;   // d itself: 16 bytes
+  g.sf_vec = g.kb % 4 == 0 && reinterpret_cast<uintptr_t>(a_scales) % 4 == 0 &&
+             reinterpret_cast<uintptr_t>(b_scales) % 4 == 0;
+  const Problem p{a_codes, b_codes, g, K, stream};
   switch (out_dtype) {
-    case FP4Q_DTYPE_BF16: return dispatch_sf<kDtBf16>(scale_format, a_codes, b_codes, g, K, stream);
-    case FP4Q_DTYPE_FP16: return dispatch_sf<kDtFp16>(scale_format, a_codes, b_codes, g, K, stream);
-    default: return dispatch_sf<kDtF32>(scale_format, a_codes, b_codes, g, K, stream);
+    case FP4Q_DTYPE_BF16: return dispatch_sf<kDtBf16>(scale_format, p);
+    case FP4Q_DTYPE_FP16: return dispatch_sf<kDtFp16>(scale_format, p);
+    default: return dispatch_sf<kDtF32>(scale_format, p);
   }
 }
 
