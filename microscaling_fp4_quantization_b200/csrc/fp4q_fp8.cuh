@@ -138,59 +138,49 @@ struct Fp8QuantArgs {
 //
 // One pass: eight lanes hold a block (16 channels each, two 16-byte loads and one 16-byte store),
 // its maximum takes three shuffles, and a warp's four blocks are neighbours in memory.  The floor
-// is the traffic, 3 bytes an element; two blocks per group of lanes are loaded before either is
-// used, which keeps 64 bytes a thread in flight.
+// is the traffic, 3 bytes an element.  A CTA does 32 blocks and leaves: the next one's loads start
+// as soon as there is room, where the CTAs of a persistent grid load and store in step.  32768 x 14336
+// bf16: 198 us, 7.1 TB/s, against 251 us on a persistent grid of one wave and 228 us with two waves of
+// four blocks to a group of lanes.
 constexpr int kFp8QuantThreads = 256;
-constexpr int kFp8QuantUnroll = 2;
+
+template <int DT>
+__device__ __forceinline__ void load_chunk(const uint16_t* p, uint32_t (&w)[8]) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  const uint4 v0 = q[0], v1 = q[1];
+  w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w;
+  w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
+}
 
 template <int DT, int SF>
 __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_rows_kernel(Fp8QuantArgs a) {
-  constexpr int U = kFp8QuantUnroll;
   pdl_launch_dependents();
   pdl_wait();
-  const uint32_t lane = threadIdx.x & 31u, sub = lane & (kFp8Lanes - 1);
-  const uint32_t warp0 = (blockIdx.x * kFp8QuantThreads + threadIdx.x) >> 5;
-  const uint64_t stride = static_cast<uint64_t>(gridDim.x) * (kFp8QuantThreads / 32) * 4;   // blocks per step of the grid
-  for (uint64_t b0 = static_cast<uint64_t>(warp0) * 4; b0 < a.n_blocks; b0 += U * stride) {
-    uint32_t w[U][8];
-    int64_t out[U];   // offset of this lane's codes, -1: no chunk here
-    uint32_t blk[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint64_t b = b0 + u * stride + (lane >> 3);
-      out[u] = -1;
-      blk[u] = static_cast<uint32_t>(b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[u][i] = 0u;
-      if (b < a.n_blocks) {
-        const uint32_t row = a.kb.div(blk[u]);
-        const int64_t col = static_cast<int64_t>(blk[u] - row * a.kb.d) * kFp8Block + sub * kFp8Chunk;
-        if (col < a.K) {
-          const uint4* p = reinterpret_cast<const uint4*>(a.x + row * a.ldx + col);
-          const uint4 v0 = __ldg(p), v1 = __ldg(p + 1);
-          w[u][0] = v0.x, w[u][1] = v0.y, w[u][2] = v0.z, w[u][3] = v0.w;
-          w[u][4] = v1.x, w[u][5] = v1.y, w[u][6] = v1.z, w[u][7] = v1.w;
-          out[u] = row * a.K + col;
-        }
-      }
+  const uint32_t sub = threadIdx.x & (kFp8Lanes - 1);
+  const uint32_t block = blockIdx.x * (kFp8QuantThreads / kFp8Lanes) + threadIdx.x / kFp8Lanes;
+  uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  int64_t out = -1;   // offset of this lane's codes; none past the end of the row or of the blocks
+  if (block < a.n_blocks) {
+    const uint32_t row = a.kb.div(block);
+    const int64_t col = static_cast<int64_t>(block - row * a.kb.d) * kFp8Block + sub * kFp8Chunk;
+    if (col < a.K) {
+      load_chunk<DT>(a.x + row * a.ldx + col, w);
+      out = row * a.K + col;
     }
+  }
+  uint32_t m = 0u;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t m = 0u;
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, pair_abs(w[i]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, pair_abs(w[u][i]));
+  for (int d = 1; d < kFp8Lanes; d *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  const Fp8Scale<SF> sc(half_bits_to_f32<DT>(max(m & 0xFFFFu, m >> 16)));
+  if (out >= 0) {
+    uint32_t c[4];
 #pragma unroll
-      for (int d = 1; d < kFp8Lanes; d *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-      const Fp8Scale<SF> sc(half_bits_to_f32<DT>(max(m & 0xFFFFu, m >> 16)));
-      if (out[u] >= 0) {
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[i] = e4m3x4(sc.quotient(pair_to_f32<DT>(w[u][2 * i])), sc.quotient(pair_to_f32<DT>(w[u][2 * i + 1])));
-        stg128(a.codes + out[u], c[0], c[1], c[2], c[3]);
-        if (sub == 0) sc.store(a.scales, blk[u]);
-      }
-    }
+    for (int i = 0; i < 4; ++i)
+      c[i] = e4m3x4(sc.quotient(pair_to_f32<DT>(w[2 * i])), sc.quotient(pair_to_f32<DT>(w[2 * i + 1])));
+    stg128(a.codes + out, c[0], c[1], c[2], c[3]);
+    if (sub == 0) sc.store(a.scales, block);
   }
 }
 
@@ -215,12 +205,7 @@ __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_tiles_kernel(Fp
     const int64_t row = row0 + i * (kFp8QuantThreads / kFp8Lanes);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = 0u;
-    if (row < a.M && col < a.K) {
-      const uint4* p = reinterpret_cast<const uint4*>(a.x + row * a.ldx + col);
-      const uint4 v0 = __ldg(p), v1 = __ldg(p + 1);
-      w[i][0] = v0.x, w[i][1] = v0.y, w[i][2] = v0.z, w[i][3] = v0.w;
-      w[i][4] = v1.x, w[i][5] = v1.y, w[i][6] = v1.z, w[i][7] = v1.w;
-    }
+    if (row < a.M && col < a.K) load_chunk<DT>(a.x + row * a.ldx + col, w[i]);
   }
   uint32_t m = 0u;
 #pragma unroll
@@ -252,7 +237,10 @@ __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_tiles_kernel(Fp
 //   h = x + r,  stored = RN(h),  y = h * (1 / sqrt(mean(h^2) + eps)) * w,  then codes and scales of y.
 //
 // A CTA takes whole rows, one after another, and holds a row in registers between its one read and
-// its one write: C chunks of 16 channels a thread.  h, the square sum (per thread in order, then over
+// its one write: C chunks of 16 channels a thread.  C = 2 where there are many rows (smaller CTAs, more
+// of them on an SM in different phases: 16384 x 8192 bf16 takes 146 us, 6.4 TB/s, against 156 us with
+// C = 1 and 182 us with C = 4); C = 1 where a row has an SM to itself and its latency counts (1 x 4096:
+// 2.3 us against 3.0).  h, the square sum (per thread in order, then over
 // lanes and warps) and y stay in fp32: y is rounded once, to its code, and the norm is of h as it was
 // before it is rounded to be stored.
 struct Fp8NormArgs {
@@ -267,15 +255,7 @@ struct Fp8NormArgs {
   float eps;
 };
 
-template <int DT>
-__device__ __forceinline__ void load_chunk(const uint16_t* p, uint32_t (&w)[8]) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-  const uint4 v0 = q[0], v1 = q[1];
-  w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w;
-  w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
-}
-
-constexpr int kFp8NormThreads = 512;   // at most; K / (16 C) rounded up to whole warps
+constexpr int kFp8NormThreads = 1024;   // at most; K / (16 C) rounded up to whole warps
 
 template <int DT, int SF, int C, bool RES>
 __global__ void __launch_bounds__(kFp8NormThreads) add_rmsnorm_fp8_kernel(Fp8NormArgs a) {

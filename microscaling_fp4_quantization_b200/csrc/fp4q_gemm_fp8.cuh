@@ -95,14 +95,18 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// E8M0 byte -> fp32: 0 is 2^-127 (a subnormal), 255 NaN.
-__device__ __forceinline__ float e8m0_value(uint32_t b) {
-  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
+// A scale as it lies in memory, and its value.  They are apart so that a loaded scale stays untouched
+// until its block is added: converting it where it is loaded would wait for the load.
+template <int SF>
+__device__ __forceinline__ uint32_t load_scale(const void* scales, int64_t i) {
+  if constexpr (SF == kSfF32) return __ldg(static_cast<const uint32_t*>(scales) + i);
+  return __ldg(static_cast<const uint8_t*>(scales) + i);
 }
 template <int SF>
-__device__ __forceinline__ float load_scale(const void* scales, int64_t i) {
-  if constexpr (SF == kSfF32) return __ldg(static_cast<const float*>(scales) + i);
-  return e8m0_value(__ldg(static_cast<const uint8_t*>(scales) + i));
+__device__ __forceinline__ float scale_value(uint32_t w) {
+  if constexpr (SF == kSfF32) return __uint_as_float(w);
+  // E8M0: byte 0 is 2^-127 (a subnormal), 255 NaN
+  return __uint_as_float(w == 0u ? 0x00400000u : w == 255u ? 0x7FFFFFFFu : w << 23);
 }
 
 template <int OT>
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       const int64_t sb0 = (col0 < g.N ? col0 : g.N - 1) / kFp8Block * g.kb;
       // A block's scales are loaded two blocks ahead, into registers of their own by parity: a copy from
       // one register to the next would wait for the load
-      float sa[2], sb[2];
+      uint32_t sa[2], sb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int j = i < g.kb ? i : 0;
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           ok = warp_wait(acc_full(u.i), u.parity, 1);
           if (!ok) break;
           tc_fence_after();
-          const float s = sa[i] * sb[i];
+          const float s = scale_value<Cfg::kSf>(sa[i]) * scale_value<Cfg::kSf>(sb[i]);
           const int j2 = jj + i + 2 < g.kb ? jj + i + 2 : g.kb - 1;
           sa[i] = load_scale<Cfg::kSf>(g.a_scales, sa0 + j2);
           sb[i] = load_scale<Cfg::kSf>(g.b_scales, sb0 + j2);
@@ -755,7 +759,7 @@ struct GemmFp8FewConfig {
   static constexpr int kTok = kBT / kHalves;                         // tokens per adding warp
   static constexpr int kAddWarp0 = 4, kAddWarps = 4 * kHalves;
   static constexpr int kThreads = 32 * (kAddWarp0 + kAddWarps);
-  static constexpr int kSumBytes = kBT * 128 * 4;                    // one tile's sums
+  static constexpr int kSumBytes = (kBT + kMaxSplit - 1) * 128 * 4;  // split x few_own rows of sums, at most
   static constexpr int kMultBytes = kAddWarps * 2 * kTok * 4;        // per adding warp: two blocks' multipliers
   static constexpr int kStages = (222 * 1024 - kSumBytes - kMultBytes) / kStageBytes;
   static constexpr int kBarOffset = kStages * kStageBytes;
@@ -769,26 +773,25 @@ struct GemmFp8FewConfig {
   static_assert(8 * (2 * kStages + 2 * kAccs) <= 512 && kSumOffset % 16 == 0 && kSmemBytes <= 227 * 1024);
 };
 
-// One thread's sums to the CTAs that own their tokens (token i: CTA i / (BT / SPLIT)), as
-// sums[rank][token of the owner][row nl].  SPLIT is a constant so that nothing is divided: with a
-// variable one the 64 stores of a thread took 6.7 us.
+// Tokens whose sums one CTA of a cluster takes.
+__host__ __device__ constexpr int few_own(int bt, int split) { return (bt + split - 1) / split; }
+
+// One thread's sums to the CTAs that own their tokens (token i: CTA i / own), as
+// sums[rank][token of the owner][row nl].  SPLIT is a constant so that the division is one by a
+// constant: with a variable one the 64 stores of a thread took 6.7 us.
 template <int SPLIT, int BT, int TOK>
 __device__ __forceinline__ void few_push(const f32x2 (&acc)[TOK / 2], uint32_t sums, int rank, int tok0, int nl) {
-  constexpr int OWN = BT / SPLIT, PER = OWN < TOK ? OWN : TOK;   // tokens of one owner in this thread
+  constexpr int OWN = few_own(BT, SPLIT);
 #pragma unroll
-  for (int o = 0; o < TOK / PER; ++o) {
-    const int tok = tok0 + o * PER, owner = tok / OWN;
+  for (int i = 0; i < TOK; ++i) {
+    float v[2];
+    f2_unpack(acc[i / 2], v[0], v[1]);
+    const int tok = tok0 + i, owner = tok / OWN;
     const uint32_t local = sums + 4u * ((rank * OWN + (tok - owner * OWN)) * 128 + nl);
-    const uint32_t to = SPLIT > 1 ? cluster_map(local, owner) : local;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      float v[2];
-      f2_unpack(acc[(o * PER + i) / 2], v[0], v[1]);
-      if constexpr (SPLIT > 1)
-        st_cluster_f32(to + 512u * i, v[i & 1]);
-      else
-        sts32(to + 512u * i, __float_as_uint(v[i & 1]));
-    }
+    if constexpr (SPLIT > 1)
+      st_cluster_f32(cluster_map(local, owner), v[i & 1]);
+    else
+      sts32(local, __float_as_uint(v[i & 1]));
   }
 }
 
@@ -838,7 +841,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   const int j0 = static_cast<int>(static_cast<int64_t>(g.kb) * rank / split);
   const int j1 = static_cast<int>(static_cast<int64_t>(g.kb) * (rank + 1) / split);
   const int64_t m0 = static_cast<int64_t>(tm) * BT, n0 = static_cast<int64_t>(tn) * 128;
-  const int own = BT / split;   // tokens whose sums this CTA takes: rank * own ...
+  const int own = few_own(BT, split);   // this CTA takes the sums of tokens rank * own ...
 
   if (warp == 0) {
     if (lane == 0) {
@@ -903,18 +906,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     // lane l takes tokens 32 i + l: their scales of a block and the tile's, loaded two blocks ahead (into
     // registers of their own by parity, as above), multiplied, and passed to the warp's other lanes
     // through shared memory
-    auto scales = [&](int j, float (&v)[TL], float& sb) {
+    auto scales = [&](int j, uint32_t (&v)[TL], uint32_t& sb) {
       const int jj = j < j1 ? j : (j1 > 0 ? j1 - 1 : 0);
       sb = load_scale<Cfg::kSf>(g.b_scales, sb0 + jj);
 #pragma unroll
       for (int i = 0; i < TL; ++i) v[i] = load_scale<Cfg::kSf>(g.a_scales, sa0[i] + jj);
     };
-    auto put = [&](int slot, const float (&v)[TL], float sb) {
+    auto put = [&](int slot, const uint32_t (&v)[TL], uint32_t sb) {
 #pragma unroll
       for (int i = 0; i < TL; ++i)
-        if (32 * i + lane < TOK) sts32(mult + 4u * (slot * TOK + 32 * i + lane), __float_as_uint(v[i] * sb));
+        if (32 * i + lane < TOK) sts32(mult + 4u * (slot * TOK + 32 * i + lane), __float_as_uint(scale_value<Cfg::kSf>(v[i]) * scale_value<Cfg::kSf>(sb)));
     };
-    float sa[2][TL], sb[2];
+    uint32_t sa[2][TL], sb[2];
     scales(j0, sa[0], sb[0]);
     scales(j0 + 1, sa[1], sb[1]);
     f32x2 acc[TOK / 2];
@@ -954,7 +957,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     if (split > 1) cluster_wait();
     switch (split) {
       case 8: few_push<8, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      case 7: few_push<7, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      case 6: few_push<6, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      case 5: few_push<5, BT, TOK>(acc, sums, rank, tok0, nl); break;
       case 4: few_push<4, BT, TOK>(acc, sums, rank, tok0, nl); break;
+      case 3: few_push<3, BT, TOK>(acc, sums, rank, tok0, nl); break;
       case 2: few_push<2, BT, TOK>(acc, sums, rank, tok0, nl); break;
       default: few_push<1, BT, TOK>(acc, sums, rank, tok0, nl); break;
     }
@@ -968,8 +975,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
   }
   // eight neighbouring columns of one token a thread: 16-byte reads and stores
   for (int c = tid; c < own * 16; c += Cfg::kThreads) {
-    const int64_t m = m0 + rank * own + c / 16, n = n0 + 8 * (c % 16);
-    if (m >= g.M || n >= g.N) continue;
+    const int tok = rank * own + c / 16;
+    const int64_t m = m0 + tok, n = n0 + 8 * (c % 16);
+    if (tok >= BT || m >= g.M || n >= g.N) continue;
     f32x2 v[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
     for (int r = 0; r < split; ++r) {

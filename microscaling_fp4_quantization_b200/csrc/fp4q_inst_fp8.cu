@@ -40,15 +40,9 @@ fp4q_status launch_quantize_fp8(int scale_format, int dtype, int block_rows, con
   return with_types(dtype, scale_format, [&]<int DT, int SF>() -> fp4q_status {
     cudaError_t e;
     if (block_rows == 1) {
-      auto kernel = quantize_fp8_rows_kernel<DT, SF>;
-      KernelInfo ki;
-      fp4q_status st = kernel_info(kernel, 0, kFp8QuantThreads, &ki, 0, -1);
-      if (st != FP4Q_OK) return st;
-      constexpr int64_t per_cta = kFp8QuantThreads / kFp8Lanes;   // blocks per step
-      int64_t ctas = (a.n_blocks + per_cta - 1) / per_cta;
-      const int64_t wave = static_cast<int64_t>(ki.sm_count) * ki.ctas_per_sm;
-      if (ctas > wave) ctas = wave;
-      e = launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kFp8QuantThreads), 0, stream, a);
+      constexpr uint32_t per_cta = kFp8QuantThreads / kFp8Lanes;   // blocks
+      e = launch_pdl(quantize_fp8_rows_kernel<DT, SF>, dim3((a.n_blocks + per_cta - 1) / per_cta),
+                     dim3(kFp8QuantThreads), 0, stream, a);
     } else {
       e = launch_pdl(quantize_fp8_tiles_kernel<DT, SF>, dim3(a.n_blocks), dim3(kFp8QuantThreads), 0, stream, a);
     }
@@ -72,28 +66,29 @@ fp4q_status launch_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, i
   a.kb = static_cast<int>((K + kFp8Block - 1) / kFp8Block);
   a.eps = eps;
   const int chunks = static_cast<int>(K / kFp8Chunk);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  const int per_thread = M <= sms && chunks <= kFp8NormThreads ? 1 : 2;   // see the kernel
   auto launch = [&]<int DT, int SF, int C, bool RES>() -> fp4q_status {
     auto kernel = add_rmsnorm_fp8_kernel<DT, SF, C, RES>;
     const int threads = ((chunks + C - 1) / C + 31) / 32 * 32;
     KernelInfo ki;
     fp4q_status st = kernel_info(kernel, 0, threads, &ki, 0, -1);
     if (st != FP4Q_OK) return st;
-    int64_t ctas = static_cast<int64_t>(ki.sm_count) * ki.ctas_per_sm;
+    int64_t ctas = 2 * static_cast<int64_t>(ki.sm_count) * ki.ctas_per_sm;   // two waves: their ends overlap
     if (ctas > M) ctas = M;
     cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(threads), 0, stream, a);
     if (e != cudaSuccess) return cuda_fail(e, "add_rmsnorm_fp8 launch");
     return FP4Q_OK;
   };
   return with_types(dtype, scale_format, [&]<int DT, int SF>() -> fp4q_status {
-    // the fewest chunks per thread that a CTA's threads hold the row with
-    if (residual) {
-      if (chunks <= kFp8NormThreads) return launch.template operator()<DT, SF, 1, true>();
-      if (chunks <= 2 * kFp8NormThreads) return launch.template operator()<DT, SF, 2, true>();
-      return launch.template operator()<DT, SF, 4, true>();
-    }
-    if (chunks <= kFp8NormThreads) return launch.template operator()<DT, SF, 1, false>();
-    if (chunks <= 2 * kFp8NormThreads) return launch.template operator()<DT, SF, 2, false>();
-    return launch.template operator()<DT, SF, 4, false>();
+    if (residual)
+      return per_thread == 1 ? launch.template operator()<DT, SF, 1, true>()
+                             : launch.template operator()<DT, SF, 2, true>();
+    return per_thread == 1 ? launch.template operator()<DT, SF, 1, false>()
+                           : launch.template operator()<DT, SF, 2, false>();
   });
 }
 

@@ -94,9 +94,10 @@ fp4q_status launch_few(Problem p, int split) {
   KernelInfo ki;
   st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki, 0, 100, split);
   if (st != FP4Q_OK) return st;
-  // a cluster takes `split` SMs of one GPC: where they do not all fit at once, split less
+  // a cluster takes `split` SMs of one GPC, and GPCs differ: where the clusters do not all fit at once,
+  // split less
   while (split > 1 && tiles > ki.max_clusters) {
-    split /= 2;
+    --split;
     st = kernel_info(kernel, Cfg::kSmemBytes, Cfg::kThreads, &ki, 0, 100, split);
     if (st != FP4Q_OK) return st;
   }
@@ -126,9 +127,11 @@ Estimate estimate(const Variant& v, const GemmFp8Args& g, int sms, bool may_spli
   const int64_t tiles = ((g.M + v.tile_m - 1) / v.tile_m) * ((g.N + v.tile_n - 1) / v.tile_n);
   const int64_t at_once = sms / v.ctas;
   const int64_t rounds = (tiles + at_once - 1) / at_once;
-  int split = 1;
-  while (may_split && split < 8 && tiles * 2 * split <= at_once && g.kb >= 4 * split) split *= 2;
-  return {v.start + (split > 1 ? 40 : 0) + rounds * ((g.kb + split - 1) / split) * v.block, split};
+  // the blocks of K over as many CTAs as there are SMs for, two at least to each
+  int64_t split = may_split ? at_once / tiles : 1;
+  if (split > g.kb / 2) split = g.kb / 2;
+  split = split < 1 ? 1 : split > 8 ? 8 : split;
+  return {v.start + (split > 1 ? 40 : 0) + rounds * ((g.kb + split - 1) / split) * v.block, static_cast<int>(split)};
 }
 
 template <int OT, int SF>
