@@ -437,6 +437,42 @@ fp4q_status noalloc_scratch(float** out) {
 
 }  // namespace
 
+namespace {
+
+// The first and one-past-last byte of `rows` rows of K elements, ld elements apart.
+struct ByteRange {
+  uintptr_t lo, hi;
+  ByteRange(const void* p, int64_t rows, int64_t K, int64_t ld, int64_t esize)
+      : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + static_cast<uintptr_t>(((rows - 1) * ld + K) * esize) : lo) {}
+  bool overlaps(const ByteRange& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Shape rules of the 8-bit quantizing calls: rows of K 16-bit elements, ld apart.
+fp4q_status check_fp8_rows(int64_t M, int64_t K, int64_t ld) {
+  if (M < 0 || K < 0 || K % 16 != 0 || K > (int64_t(1) << 31) - 128) return FP4Q_ERR_SHAPE;
+  if (ld < K || ld % 8 != 0) return FP4Q_ERR_SHAPE;
+  if (K > 0 && M > ((int64_t(1) << 31) - 1) / ((K + 127) / 128)) return FP4Q_ERR_SHAPE;
+  if (M > 0 && ld > (int64_t(1) << 40) / M) return FP4Q_ERR_SHAPE;
+  return FP4Q_OK;
+}
+
+// No C++ exception crosses the ABI: the launchers keep tables that can run out of memory.
+template <class F>
+fp4q_status no_throw(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    std::snprintf(last_error_buffer(), kLastErrorBytes, "out of host memory");
+    return FP4Q_ERR_CUDA;
+  }
+}
+
+bool valid_fp8_scale(int f) { return f == FP4Q_FP8_SCALE_F32 || f == FP4Q_FP8_SCALE_E8M0; }
+uintptr_t fp8_scale_align(int f) { return f == FP4Q_FP8_SCALE_F32 ? 4 : 1; }
+int64_t fp8_scale_bytes(int f) { return f == FP4Q_FP8_SCALE_F32 ? 4 : 1; }
+
+}  // namespace
+
 extern "C" {
 
 fp4q_status fp4q_rotate_quantize_nvfp4_dynamic_noalloc(const void* x_bf16, int64_t M, int64_t K, int hadamard_block,
@@ -796,31 +832,6 @@ fp4q_status fp4q_gemm(int format, const void* a_codes, const void* a_scales, con
   return launch_gemm<kNV>(ac, as, a_tensor_scale, bc, bs, b_tensor_scale, M, N, K, d, s);
 }
 
-namespace {
-
-// The first and one-past-last byte of `rows` rows of K elements, ld elements apart.
-struct ByteRange {
-  uintptr_t lo, hi;
-  ByteRange(const void* p, int64_t rows, int64_t K, int64_t ld, int64_t esize)
-      : lo(reinterpret_cast<uintptr_t>(p)), hi(p ? lo + static_cast<uintptr_t>(((rows - 1) * ld + K) * esize) : lo) {}
-  bool overlaps(const ByteRange& o) const { return lo < o.hi && o.lo < hi; }
-};
-
-// Shape rules of the 8-bit quantizing calls: rows of K 16-bit elements, ld apart.
-fp4q_status check_fp8_rows(int64_t M, int64_t K, int64_t ld) {
-  if (M < 0 || K < 0 || K % 16 != 0 || K > (int64_t(1) << 31) - 128) return FP4Q_ERR_SHAPE;
-  if (ld < K || ld % 8 != 0) return FP4Q_ERR_SHAPE;
-  if (K > 0 && M > ((int64_t(1) << 31) - 1) / ((K + 127) / 128)) return FP4Q_ERR_SHAPE;
-  if (M > 0 && ld > (int64_t(1) << 40) / M) return FP4Q_ERR_SHAPE;
-  return FP4Q_OK;
-}
-
-bool valid_fp8_scale(int f) { return f == FP4Q_FP8_SCALE_F32 || f == FP4Q_FP8_SCALE_E8M0; }
-uintptr_t fp8_scale_align(int f) { return f == FP4Q_FP8_SCALE_F32 ? 4 : 1; }
-int64_t fp8_scale_bytes(int f) { return f == FP4Q_FP8_SCALE_F32 ? 4 : 1; }
-
-}  // namespace
-
 fp4q_status fp4q_quantize_fp8(int scale_format, int dtype, int block_rows, const void* x, int64_t ldx, int64_t M,
                               int64_t K, void* codes_out, void* scales_out, void* stream) {
   if (!valid_fp8_scale(scale_format) || (dtype != FP4Q_DTYPE_BF16 && dtype != FP4Q_DTYPE_FP16) ||
@@ -836,8 +847,10 @@ fp4q_status fp4q_quantize_fp8(int scale_format, int dtype, int block_rows, const
   const ByteRange rx(x, M, K, ldx, 2), rc(codes_out, M, K, K, 1),
       rs(scales_out, rb, kb, kb, fp8_scale_bytes(scale_format));
   if (rx.overlaps(rc) || rx.overlaps(rs) || rc.overlaps(rs)) return FP4Q_ERR_ARG;
-  return launch_quantize_fp8(scale_format, dtype, block_rows, x, ldx, M, K, codes_out, scales_out,
-                             static_cast<cudaStream_t>(stream));
+  return no_throw([&] {
+    return launch_quantize_fp8(scale_format, dtype, block_rows, x, ldx, M, K, codes_out, scales_out,
+                               static_cast<cudaStream_t>(stream));
+  });
 }
 
 fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int64_t ldx, const void* residual,
@@ -867,8 +880,10 @@ fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int
   // writes it, before it does), but over neither shifted
   if (ro.overlaps(rx) && (residual_out != x || ldo != ldx)) return FP4Q_ERR_ARG;
   if (ro.overlaps(rr) && (residual_out != residual || ldo != ldr)) return FP4Q_ERR_ARG;
-  return launch_add_rmsnorm_fp8(scale_format, dtype, x, ldx, residual, ldr, weight, eps, M, K, residual_out, ldo,
-                                codes_out, scales_out, static_cast<cudaStream_t>(stream));
+  return no_throw([&] {
+    return launch_add_rmsnorm_fp8(scale_format, dtype, x, ldx, residual, ldr, weight, eps, M, K, residual_out, ldo,
+                                  codes_out, scales_out, static_cast<cudaStream_t>(stream));
+  });
 }
 
 fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
@@ -891,8 +906,10 @@ fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, 
   if (rd.overlaps(ByteRange(a_codes, M, K, K, 1)) || rd.overlaps(ByteRange(b_codes, N, K, K, 1)) ||
       rd.overlaps(ByteRange(a_scales, M, kb, kb, sb)) || rd.overlaps(ByteRange(b_scales, (N + 127) / 128, kb, kb, sb)))
     return FP4Q_ERR_ARG;
-  return launch_gemm_fp8(scale_format, out_dtype, a_codes, a_scales, b_codes, b_scales, M, N, K, d,
-                         static_cast<cudaStream_t>(stream));
+  return no_throw([&] {
+    return launch_gemm_fp8(scale_format, out_dtype, a_codes, a_scales, b_codes, b_scales, M, N, K, d,
+                           static_cast<cudaStream_t>(stream));
+  });
 }
 
 fp4q_status fp4q_selftest_wait_timeout(void* stream) {

@@ -2,6 +2,8 @@
 // the library's kernels compile in parallel (see fp4q_host.cuh).
 #include "fp4q_gemm_fp8.cuh"
 
+#include <atomic>
+
 #include "fp4q_launch.cuh"
 
 namespace fp4q {
@@ -61,13 +63,16 @@ fp4q_status launch_many(Kernel kernel, Problem p) {
 template <class Cfg, class Kernel>
 fp4q_status check_registers(Kernel kernel) {
   if constexpr (Cfg::kRegSplit) {
-    static const int regs = [&] {
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_relaxed) == 0) {
       cudaFuncAttributes fa = {};
-      return cudaFuncGetAttributes(&fa, kernel) == cudaSuccess ? fa.numRegs : 0;
-    }();
-    if (regs < Cfg::kRegsLaunch) {
-      std::snprintf(last_error_buffer(), kLastErrorBytes, "gemm_fp8: built with %d registers a thread, not %d", regs,
-                    Cfg::kRegsLaunch);
+      cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+      regs.store(fa.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < Cfg::kRegsLaunch) {
+      std::snprintf(last_error_buffer(), kLastErrorBytes, "gemm_fp8: built with %d registers a thread, not %d",
+                    regs.load(), Cfg::kRegsLaunch);
       return FP4Q_ERR_UNSUPPORTED;
     }
   }
@@ -107,17 +112,23 @@ fp4q_status launch_few(Problem p, int split) {
   return FP4Q_OK;
 }
 
-// Which kernel: the one whose time, as a start and a number of blocks of K worked off one after another,
-// comes out least.  Starts and times per block (in units of 10 ns) are those measured on 148 SMs, with
-// operands in L2: see the table in the design notes for both sides of each choice.
+// Which kernel: the one whose time comes out least, as a start, a cost for each round of tiles over the
+// SMs, and one for each block of K that a round works off (units of 10 ns).  The costs are fitted to
+// measurements of all four kernels at M = 1 ... 4096 and nine pairs of N and K (1024 x 4096 to
+// 8192 x 8192, 600 x 784): over those the choice takes 0.7 % longer than the fastest of the four on
+// average (1.7 % with one cost per block alone).  Examples, in us as few / 128 x 128 / 256 x 128 / wide:
+// 96 x 8192 x 8192 25.6 / 24.6 / 23.7 / 34.5; 333 x 4104 x 5008 31.3 / 20.4 / 17.8 / 24.4; 256 x 4096 x
+// 4096 13.5 / 13.9 / 13.6 / 20.4; 1024 x 4096 x 4096 E8M0 49.4 / 27.3 / 27.9 / 22.7.
 struct Variant {
   int tile_m, tile_n;   // of D
   int ctas;             // per tile
-  int start, block;
+  int start, round, block;
 };
-constexpr Variant kFew16{16, 128, 1, 330, 22}, kFew32{32, 128, 1, 330, 26}, kFew64{64, 128, 1, 330, 30},
-    kOne128{128, 128, 1, 450, 31}, kPair128{256, 128, 2, 450, 30}, kPair256{256, 256, 2, 450, 52},
-    kPairMx{256, 224, 2, 450, 31};
+constexpr Variant kFew16{16, 128, 1, 250, 60, 36}, kFew32{32, 128, 1, 250, 110, 31}, kFew64{64, 128, 1, 170, 250, 31};
+// by scale format: with E8M0 the widest tile has its scales applied by the tensor core
+constexpr Variant kOne[2] = {{128, 128, 1, 300, 140, 32}, {128, 128, 1, 280, 140, 33}};
+constexpr Variant kPair[2] = {{256, 128, 2, 320, 130, 30}, {256, 128, 2, 340, 120, 34}};
+constexpr Variant kWide[2] = {{256, 256, 2, 430, 150, 48}, {256, 224, 2, 470, 90, 30}};
 
 struct Estimate {
   int64_t time;
@@ -131,7 +142,8 @@ Estimate estimate(const Variant& v, const GemmFp8Args& g, int sms, bool may_spli
   int64_t split = may_split ? at_once / tiles : 1;
   if (split > g.kb / 2) split = g.kb / 2;
   split = split < 1 ? 1 : split > 8 ? 8 : split;
-  return {v.start + (split > 1 ? 40 : 0) + rounds * ((g.kb + split - 1) / split) * v.block, static_cast<int>(split)};
+  return {v.start + (split > 1 ? 40 : 0) + rounds * (v.round + (g.kb + split - 1) / split * v.block),
+          static_cast<int>(split)};
 }
 
 template <int OT, int SF>
@@ -142,8 +154,8 @@ fp4q_status dispatch(const Problem& p) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
   const GemmFp8Args& g = p.g;
   const Estimate few = estimate(g.M <= 16 ? kFew16 : g.M <= 32 ? kFew32 : kFew64, g, sms, true);
-  const int64_t one = estimate(kOne128, g, sms, false).time, pair = estimate(kPair128, g, sms, false).time;
-  const int64_t wide = estimate(SF == kSfE8m0 ? kPairMx : kPair256, g, sms, false).time;
+  const int64_t one = estimate(kOne[SF], g, sms, false).time, pair = estimate(kPair[SF], g, sms, false).time;
+  const int64_t wide = estimate(kWide[SF], g, sms, false).time;
   if (few.time <= one && few.time <= pair && few.time <= wide) {
     if (g.M <= 16) return launch_few<GemmFp8FewConfig<16, OT, SF>>(p, few.split);
     if (g.M <= 32) return launch_few<GemmFp8FewConfig<32, OT, SF>>(p, few.split);
