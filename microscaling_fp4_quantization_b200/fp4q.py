@@ -286,66 +286,67 @@ def quant_error(plan: Plan, x, tensor_scale=None, stream=None):
 
 # ---- 8-bit linear layers.  Codes are torch.float8_e4m3fn tensors, scales float32 or torch.float8_e8m0fnu
 # ones.  The calls run on the tensors' device, on its current stream unless one is given.  The checks are
-# kept short: at one token a call costs the host more than it costs the GPU.
+# written for few attribute reads: at one token a call costs the host more than it costs the GPU.
 
 _torch = None            # set by the first call: importing this module does not import torch
-_fp8_dtype_codes: dict = {}
+_e4m3 = None
+_raw_stream = None       # device index -> handle of its current stream (current_stream() takes 3 us to say it)
+_current_device = None
+_fp8_in_dtypes: dict = {}      # input types, and their codes
+_fp8_out_dtypes: dict = {}
 _fp8_scale_dtypes: dict = {}
 
 
 def _fp8_init() -> None:
-    global _torch
+    global _torch, _e4m3, _raw_stream, _current_device
     import torch
-    _fp8_dtype_codes.update({torch.bfloat16: FP4Q_DTYPE_BF16, torch.float16: FP4Q_DTYPE_FP16,
-                             torch.float32: FP4Q_DTYPE_F32})
+    _fp8_in_dtypes.update({torch.bfloat16: FP4Q_DTYPE_BF16, torch.float16: FP4Q_DTYPE_FP16})
+    _fp8_out_dtypes.update(_fp8_in_dtypes)
+    _fp8_out_dtypes[torch.float32] = FP4Q_DTYPE_F32
     _fp8_scale_dtypes.update({FP4Q_FP8_SCALE_F32: torch.float32, FP4Q_FP8_SCALE_E8M0: torch.float8_e8m0fnu})
+    _e4m3 = torch.float8_e4m3fn
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _current_device = torch.cuda.current_device
     _torch = torch
 
 
-def _fp8_rows(name: str, t, like=None) -> int:
-    """Check a 2-D tensor of rows whose elements are neighbours, and against x (like) if one is given;
-    returns the distance between rows."""
-    shape, ld = t.shape, 0
-    if t.is_cuda and len(shape) == 2 and _fp8_dtype_codes.get(t.dtype, FP4Q_DTYPE_F32) != FP4Q_DTYPE_F32:
-        if shape[0] <= 1 or shape[1] == 0:
-            ld = shape[1]
-        else:
-            ld = t.stride(0)
-        if shape[1] > 1 and t.stride(1) != 1:
-            ld = -1
-    else:
-        ld = -1
-    if ld < 0:
-        raise ValueError(f"{name} must be a 2-D bf16 or fp16 CUDA tensor whose rows are contiguous")
-    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+def _fp8_ld(name: str, t) -> int:
+    """The distance between the rows of a 2-D tensor whose rows are contiguous."""
+    M, K = t.shape
+    if K > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0) if M > 1 and K > 0 else K
+
+
+def _fp8_like(name: str, t, shape, dtype, index) -> int:
+    """Check a tensor that goes with x; returns the distance between its rows."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
         raise ValueError(f"{name} must match x in shape, dtype and device")
-    return ld
+    return shape[1] if t.is_contiguous() else _fp8_ld(name, t)
 
 
-def _fp8_buffer(name: str, t, shape, dtype, device):
-    """A given output after checking it, or a new one."""
-    if t is None:
-        return _torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+def _fp8_array(name: str, t, shape, dtype, index):
+    """Check a contiguous tensor."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {index}")
     return t
 
 
-def _fp8_call(name: str, device, stream, *args) -> None:
+def _fp8_call(name: str, index: int, stream, *args) -> None:
     """The C call `name` on the device's current stream, or on the given one, with the device current."""
-    index = device.index
     if stream is None:
-        stream = _torch._C._cuda_getCurrentRawStream(index)   # current_stream() takes 3 us to say the same
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on CUDA device {index}")
         stream = stream.cuda_stream
-    if _torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = getattr(_lib, name)(*args, stream)
     else:
         with _torch.cuda.device(index):
             status = getattr(_lib, name)(*args, stream)
-    _check(status, name)
+    if status:
+        raise Fp4qError(status, name)
 
 
 def quantize_fp8(x, block_rows: int = 1, scale_format: int = FP4Q_FP8_SCALE_F32, codes=None, scales=None, stream=None):
@@ -355,15 +356,21 @@ def quantize_fp8(x, block_rows: int = 1, scale_format: int = FP4Q_FP8_SCALE_F32,
     FP4Q_FP8_SCALE_E8M0 (float8_e8m0fnu).  codes, scales: outputs to write into."""
     if _torch is None:
         _fp8_init()
-    ldx = _fp8_rows("x", x)
-    if block_rows not in (1, 128) or scale_format not in _fp8_scale_dtypes:
+    shape, dtype, index = x.shape, _fp8_in_dtypes.get(x.dtype), x.get_device()
+    if dtype is None or index < 0 or len(shape) != 2:
+        raise ValueError("x must be a 2-D bf16 or fp16 CUDA tensor")
+    s_dtype = _fp8_scale_dtypes.get(scale_format)
+    if s_dtype is None or block_rows not in (1, 128):
         raise ValueError("block_rows must be 1 or 128 and scale_format one of FP4Q_FP8_SCALE_*")
-    M, K = x.shape
-    device = x.device
-    codes = _fp8_buffer("codes", codes, (M, K), _torch.float8_e4m3fn, device)
-    scales = _fp8_buffer("scales", scales, (-(-M // block_rows), -(-K // 128)), _fp8_scale_dtypes[scale_format], device)
-    _fp8_call("fp4q_quantize_fp8", device, stream, scale_format, _fp8_dtype_codes[x.dtype], block_rows, x.data_ptr(),
-              ldx, M, K, codes.data_ptr(), scales.data_ptr())
+    M, K = shape
+    ldx = K if x.is_contiguous() else _fp8_ld("x", x)
+    s_shape = (-(-M // block_rows), -(-K // 128))
+    codes = _torch.empty(shape, dtype=_e4m3, device=x.device) if codes is None else \
+        _fp8_array("codes", codes, shape, _e4m3, index)
+    scales = _torch.empty(s_shape, dtype=s_dtype, device=x.device) if scales is None else \
+        _fp8_array("scales", scales, s_shape, s_dtype, index)
+    _fp8_call("fp4q_quantize_fp8", index, stream, scale_format, dtype, block_rows, x.data_ptr(), ldx, M, K,
+              codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -375,29 +382,34 @@ def add_rmsnorm_fp8(x, residual, weight, eps: float, scale_format: int = FP4Q_FP
     be given: residual or x itself, or another tensor that overlaps neither."""
     if _torch is None:
         _fp8_init()
-    ldx = _fp8_rows("x", x)
-    M, K = x.shape
-    device, dtype = x.device, x.dtype
-    if scale_format not in _fp8_scale_dtypes:
+    shape, t_dtype, index = x.shape, x.dtype, x.get_device()
+    dtype, s_dtype = _fp8_in_dtypes.get(t_dtype), _fp8_scale_dtypes.get(scale_format)
+    if dtype is None or index < 0 or len(shape) != 2:
+        raise ValueError("x must be a 2-D bf16 or fp16 CUDA tensor")
+    if s_dtype is None:
         raise ValueError("scale_format must be one of FP4Q_FP8_SCALE_*")
-    if weight.shape != (K,) or weight.dtype != dtype or weight.device != device or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous tensor [K] of x's dtype and device")
+    M, K = shape
+    ldx = K if x.is_contiguous() else _fp8_ld("x", x)
+    _fp8_array("weight", weight, (K,), t_dtype, index)
     ldr = ldo = K
     p_res = p_out = None
     if residual is not None:
-        ldr = _fp8_rows("residual", residual, x)
+        ldr = _fp8_like("residual", residual, shape, t_dtype, index)
         if residual_out is None:
-            residual_out = _torch.empty((M, K), dtype=dtype, device=device)
+            residual_out = _torch.empty(shape, dtype=t_dtype, device=x.device)
         else:
-            ldo = _fp8_rows("residual_out", residual_out, x)
+            ldo = _fp8_like("residual_out", residual_out, shape, t_dtype, index)
         p_res, p_out = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out goes with a residual")
-    codes = _fp8_buffer("codes", codes, (M, K), _torch.float8_e4m3fn, device)
-    scales = _fp8_buffer("scales", scales, (M, -(-K // 128)), _fp8_scale_dtypes[scale_format], device)
-    if M * K > 0:   # (an empty tensor's null pointers say nothing about a residual)
-        _fp8_call("fp4q_add_rmsnorm_fp8", device, stream, scale_format, _fp8_dtype_codes[dtype], x.data_ptr(), ldx,
-                  p_res, ldr, weight.data_ptr(), eps, M, K, p_out, ldo, codes.data_ptr(), scales.data_ptr())
+    s_shape = (M, -(-K // 128))
+    codes = _torch.empty(shape, dtype=_e4m3, device=x.device) if codes is None else \
+        _fp8_array("codes", codes, shape, _e4m3, index)
+    scales = _torch.empty(s_shape, dtype=s_dtype, device=x.device) if scales is None else \
+        _fp8_array("scales", scales, s_shape, s_dtype, index)
+    if M > 0 and K > 0:   # (an empty tensor's null pointers say nothing about a residual)
+        _fp8_call("fp4q_add_rmsnorm_fp8", index, stream, scale_format, dtype, x.data_ptr(), ldx, p_res, ldr,
+                  weight.data_ptr(), eps, M, K, p_out, ldo, codes.data_ptr(), scales.data_ptr())
     return codes, scales, residual_out
 
 
@@ -408,26 +420,25 @@ def gemm_fp8(a_codes, a_scales, b_codes, b_scales, out_dtype=None, out=None, str
     fp32.  out: a tensor to write into."""
     if _torch is None:
         _fp8_init()
-    device, s_dtype = a_codes.device, a_scales.dtype
-    if a_codes.dim() != 2 or b_codes.dim() != 2:
-        raise ValueError("a_codes [M, K] and b_codes [N, K] must be 2-D")
-    (M, K), N = a_codes.shape, b_codes.shape[0]
+    shape, b_shape, s_dtype, index = a_codes.shape, b_codes.shape, a_scales.dtype, a_codes.get_device()
+    if len(shape) != 2 or len(b_shape) != 2 or index < 0:
+        raise ValueError("a_codes [M, K] and b_codes [N, K] must be 2-D CUDA tensors")
+    (M, K), N = shape, b_shape[0]
     kb = -(-K // 128)
-    fmt = FP4Q_FP8_SCALE_F32 if s_dtype == _torch.float32 else FP4Q_FP8_SCALE_E8M0
-    if s_dtype != _fp8_scale_dtypes[fmt]:
+    fmt = FP4Q_FP8_SCALE_F32 if s_dtype is _torch.float32 else FP4Q_FP8_SCALE_E8M0
+    if s_dtype is not _fp8_scale_dtypes[fmt]:
         raise ValueError("the scales must be float32 or float8_e8m0fnu")
-    if not a_codes.is_cuda:
-        raise ValueError("the operands must be CUDA tensors")
-    e4m3 = _torch.float8_e4m3fn
-    _fp8_buffer("a_codes", a_codes, (M, K), e4m3, device)
-    _fp8_buffer("b_codes", b_codes, (N, K), e4m3, device)
-    _fp8_buffer("a_scales", a_scales, (M, kb), s_dtype, device)
-    _fp8_buffer("b_scales", b_scales, (-(-N // 128), kb), s_dtype, device)
+    _fp8_array("a_codes", a_codes, shape, _e4m3, index)
+    _fp8_array("b_codes", b_codes, (N, K), _e4m3, index)
+    _fp8_array("a_scales", a_scales, (M, kb), s_dtype, index)
+    _fp8_array("b_scales", b_scales, (-(-N // 128), kb), s_dtype, index)
     if out_dtype is None:
         out_dtype = _torch.bfloat16 if out is None else out.dtype
-    if out_dtype not in _fp8_dtype_codes:
+    dtype = _fp8_out_dtypes.get(out_dtype)
+    if dtype is None:
         raise ValueError("out_dtype must be bf16, fp16 or fp32")
-    out = _fp8_buffer("out", out, (M, N), out_dtype, device)
-    _fp8_call("fp4q_gemm_fp8", device, stream, fmt, _fp8_dtype_codes[out_dtype], a_codes.data_ptr(),
-              a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(), M, N, K, out.data_ptr())
+    out = _torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else \
+        _fp8_array("out", out, (M, N), out_dtype, index)
+    _fp8_call("fp4q_gemm_fp8", index, stream, fmt, dtype, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
+              b_scales.data_ptr(), M, N, K, out.data_ptr())
     return out
