@@ -201,6 +201,18 @@ __device__ __forceinline__ void lds_pairs(uint32_t addr, f32x2& a, f32x2& b) {
 // one fused multiply-add per element.  Persistent, round-robin over the tiles.  C = 2 pairs the CTAs
 // of a cluster on one tile (cta_group::2, M = 256): each loads its 128 rows of A and half of B's, and
 // the leader issues the MMAs of both.
+// Tile t's row and column of tiles: down kGroup rows, then the next column, so that the tiles worked on
+// at one time (74 pairs: 16 rows by 4.6 columns) share their rows of A and of B in L2.  8192^3 takes
+// 523 us with fp32 scales and 397 us with E8M0, against 555 and 440 us down all 32 rows; groups of 8 and
+// 32 rows lie between, and where A's rows are few there is no difference.
+constexpr int kTileGroup = 16;
+__device__ __forceinline__ void gemm_fp8_tile(const GemmFp8Args& g, int t, int& tm, int& tn) {
+  const int per_group = kTileGroup * g.tiles_n, group = t / per_group, in_group = t - group * per_group;
+  const int rows = min(kTileGroup, g.tiles_m - group * kTileGroup);
+  tn = in_group / rows;
+  tm = group * kTileGroup + in_group - tn * rows;
+}
+
 constexpr int kMmaTries = 64;   // times an MMA warp asks for its barriers before it suspends
 
 template <int CTAS, int BN_, int OT, int SF>
@@ -335,7 +347,8 @@ __device__ __forceinline__ void gemm_fp8_produce(const GemmFp8Args& g, const CUt
   bool ok = true;
   int filled = 0;
   for (int t = t0; ok && t < n_tiles; t += dt) {
-    const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+    int tm, tn;
+    gemm_fp8_tile(g, t, tm, tn);
     const int ra = tm * Cfg::kBM + rank * Cfg::kARows, rb = tn * Cfg::kBN + rank * Cfg::kBRows;
     for (int j = 0; j < g.kb; ++j, r.next()) {
       const uint32_t full = bars + 8u * r.i, empty = bars + 8u * (S + r.i), dst = stage0 + r.i * Cfg::kStageBytes;
@@ -458,7 +471,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     RingPos<NA> u;
     bool ok = true;
     for (int t = t0; ok && t < n_tiles; t += dt) {
-      const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+      int tm, tn;
+      gemm_fp8_tile(g, t, tm, tn);
       const int64_t row = static_cast<int64_t>(tm) * Cfg::kBM + rank * 128 + 32 * q + lane;
       const int64_t col0 = static_cast<int64_t>(tn) * BN + half * NC;
       // rows and columns past the end use the last ones' scales; they are not stored
@@ -678,7 +692,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     pdl_wait();   // D may still be read by an earlier kernel
     RingPos<2> u;
     for (int t = t0; t < n_tiles; t += dt, u.next()) {
-      const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+      int tm, tn;
+      gemm_fp8_tile(g, t, tm, tn);
       const int64_t row = static_cast<int64_t>(tm) * Cfg::kBM + rank * 128 + 32 * q + lane;
       const int64_t col0 = static_cast<int64_t>(tn) * BN + half * NC;
       if (!warp_wait(acc_full(u.i), u.parity, 0)) break;
@@ -704,7 +719,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     RingPos<2> f;
     bool ok = true;
     for (int t = t0; ok && t < n_tiles; t += dt) {
-      const int tm = t % g.tiles_m, tn = t / g.tiles_m;
+      int tm, tn;
+      gemm_fp8_tile(g, t, tm, tn);
       const int64_t ra = static_cast<int64_t>(tm) * Cfg::kBM + rank * 128 + lane;
       const int64_t rb = static_cast<int64_t>(tn) * BN + lane;
       for (int j = 0; j < g.kb; j += 4, f.next()) {
