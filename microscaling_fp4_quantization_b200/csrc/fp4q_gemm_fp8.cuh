@@ -95,6 +95,11 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Fetch a tensor map ahead of the first copy that uses it.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // A scale as it lies in memory, and its value.  They are apart so that a loaded scale stays untouched
 // until its block is added: converting it where it is loaded would wait for the load.
 template <int SF>
@@ -341,6 +346,8 @@ __device__ __forceinline__ void gemm_fp8_produce(const GemmFp8Args& g, const CUt
                                                  int rank, int t0, int dt, uint32_t stage0, uint32_t bars) {
   constexpr int S = Cfg::kStages, C = Cfg::kCtas;
   if ((threadIdx.x & 31) != 0) return;
+  prefetch_map(&amap);
+  prefetch_map(&bmap);
   pdl_wait();
   const int n_tiles = g.tiles_m * g.tiles_n;
   RingPos<S> r;
@@ -861,6 +868,8 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      prefetch_map(&wmap);
+      prefetch_map(&xmap);
       pdl_wait();
       RingPos<S> r;
       int filled = 0;
@@ -905,6 +914,11 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       u = un;
     }
     if (last) mbar_wait_bounded(acc_full((last >> 1) & 0x7F), last >> 8);
+  } else if (warp == 2) {
+    // B's first stages into L2 while the kernel in front still runs (which may even be writing them: L2 is
+    // where all copies meet, and the ring's own loads come after the wait)
+    if (lane == 0)
+      for (int j = j0; j < j1 && j < j0 + S; ++j) tma_prefetch_2d(&wmap, j * Cfg::kBK, tn * 128);
   } else if (warp >= Cfg::kAddWarp0) {
     // lane quarter warp % 4: this thread holds B's row n0 + nl and TOK of the tile's tokens, from `tok0` on
     const int q = warp & 3, nl = 32 * q + lane;
