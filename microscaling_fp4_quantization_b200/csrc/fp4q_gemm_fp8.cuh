@@ -239,7 +239,7 @@ struct GemmFp8Config {
   // 128 sums a thread need more registers than 384 threads share out evenly (168): the first four
   // warps hand theirs to the adding warps
   static constexpr bool kRegSplit = kCols == 128;
-  static constexpr int kRegsLaunch = 168, kRegsFew = 40, kRegsMany = 232;
+  static constexpr int kRegsLaunch = 168, kRegsFew = 56, kRegsMany = 224;
   static_assert(kRegsFew * kAddWarp0 + kRegsMany * kAddWarps <= kRegsLaunch * (kAddWarp0 + kAddWarps));
   static constexpr uint32_t kIdesc = gemm_fp8_idesc(kBM, kBN);
 };
@@ -301,6 +301,13 @@ __device__ __forceinline__ bool warp_wait2(uint32_t bar_a, uint32_t parity_a, ui
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar_a, parity_a) && mbar_wait_bounded(bar_b, parity_b));
 }
 
+// Blocks after which two rings are both back at their first slot.
+constexpr int ring_unroll(int a, int b) {
+  int u = a;
+  while (u % b != 0) u += a;
+  return u;
+}
+
 template <int CTAS>
 __device__ __forceinline__ void gemm_fp8_mma(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
   if constexpr (CTAS == 1) {
@@ -339,35 +346,43 @@ __device__ __forceinline__ void gemm_fp8_load(uint32_t dst, const CUtensorMap* m
   }
 }
 
-// Producer warp of the many-row kernels: this CTA's rows of A and of B, stage after stage (one lane).
-// full barriers lie at `bars`, empty ones behind them; a pair's copies complete on the leader's.
+// Producer warp of the many-row kernels: this CTA's rows of A and of B, stage after stage.  full barriers
+// lie at `bars`, empty ones behind them; a pair's copies complete on the leader's.  As in the MMA warp the
+// whole warp runs the loop, one lane issues, and a stage's barrier is asked for a stage ahead.
 template <class Cfg>
 __device__ __forceinline__ void gemm_fp8_produce(const GemmFp8Args& g, const CUtensorMap& amap, const CUtensorMap& bmap,
                                                  int rank, int t0, int dt, uint32_t stage0, uint32_t bars) {
   constexpr int S = Cfg::kStages, C = Cfg::kCtas;
-  if ((threadIdx.x & 31) != 0) return;
-  prefetch_map(&amap);
-  prefetch_map(&bmap);
+  if (elect_one()) {
+    prefetch_map(&amap);
+    prefetch_map(&bmap);
+  }
+  __syncwarp();
   pdl_wait();
   const int n_tiles = g.tiles_m * g.tiles_n;
+  const uint32_t full0 = C == 2 ? cluster_map(bars, 0) : bars;
   RingPos<S> r;
-  bool ok = true;
+  bool ok = true, ready = true;
   int filled = 0;
   for (int t = t0; ok && t < n_tiles; t += dt) {
     int tm, tn;
     gemm_fp8_tile(g, t, tm, tn);
     const int ra = tm * Cfg::kBM + rank * Cfg::kARows, rb = tn * Cfg::kBN + rank * Cfg::kBRows;
-    for (int j = 0; j < g.kb; ++j, r.next()) {
-      const uint32_t full = bars + 8u * r.i, empty = bars + 8u * (S + r.i), dst = stage0 + r.i * Cfg::kStageBytes;
-      if (!mbar_test(empty, r.parity ^ 1u) && !mbar_wait_bounded(empty, r.parity ^ 1u)) {
-        ok = false;
-        break;
+    for (int j = 0; j < g.kb; ++j) {
+      if (!__all_sync(0xFFFFFFFFu, ready)) ok = warp_wait(bars + 8u * (S + r.i), r.parity ^ 1u, 1);
+      if (!ok) break;
+      RingPos<S> rn = r;
+      rn.next();
+      ready = mbar_test(bars + 8u * (S + rn.i), rn.parity ^ 1u);
+      if (elect_one()) {
+        const uint32_t dst = stage0 + r.i * Cfg::kStageBytes, bar = full0 + 8u * r.i;
+        if (rank == 0) mbar_arrive_expect_tx(bars + 8u * r.i, C * Cfg::kStageBytes);
+        gemm_fp8_load<C>(dst, &amap, j * Cfg::kBK, ra, bar);
+        gemm_fp8_load<C>(dst + Cfg::kABytes, &bmap, j * Cfg::kBK, rb, bar);
       }
-      if (rank == 0) mbar_arrive_expect_tx(full, C * Cfg::kStageBytes);
-      const uint32_t bar = C == 2 ? cluster_map(full, 0) : full;
-      gemm_fp8_load<C>(dst, &amap, j * Cfg::kBK, ra, bar);
-      gemm_fp8_load<C>(dst + Cfg::kABytes, &bmap, j * Cfg::kBK, rb, bar);
+      __syncwarp();
       filled = filled < S ? filled + 1 : S;
+      r = rn;
     }
   }
   // every issued copy has landed once its stage was read (or, where a wait ran out, long before): the
@@ -433,41 +448,47 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
     gemm_fp8_produce<Cfg>(g, amap, bmap, rank, t0, dt, stage0, bars);
   } else if (warp == 1) {
     // ---------------- MMA issuer (a pair's leader): one K-block into one accumulator.  The whole warp
-    // runs the loop, which keeps the descriptors in uniform registers; one lane issues
+    // runs the loop, one lane issues.  The loop knows nothing of tiles and is unrolled over the rings, so
+    // that a block costs it little besides its instructions: kept rolled, it took 500 cycles a block and
+    // held up MMAs of 256.
     if (rank == 0) {
-      RingPos<S> r;
-      RingPos<NA> u;
-      bool ok = true, ready = false;
-      uint32_t last = 0;   // 1 | accumulator << 1 | parity << 8 of the last commit, 0: none
+      constexpr int U = ring_unroll(S, NA);
+      const int64_t n = t0 < n_tiles ? static_cast<int64_t>((n_tiles - t0 + dt - 1) / dt) * g.kb : 0;   // blocks
       const uint64_t da0 = umma_smem_desc(a_tile(0), 1024, 2), db0 = umma_smem_desc(b_tile(0), 1024, 2);
-      for (int t = t0; ok && t < n_tiles; t += dt) {
-        for (int j = 0; j < g.kb; ++j) {
+      bool ok = true, ready = false;
+      uint32_t pass = 0;   // over the unrolled loop, modulo 2
+#pragma unroll 1
+      for (int64_t it = 0; ok && it < n; it += U, pass ^= 1u) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          // slots and parities of this block and of the next, fixed but for the pass
+          constexpr int PF = U / S, PA = U / NA;   // passes over each ring in one over the loop
+          const int s = k % S, d = k % NA, kn = (k + 1) % U, sn = kn % S, dn = kn % NA;
+          const uint32_t pn = k + 1 == U ? pass ^ 1u : pass;
+          const uint32_t full_par = (pass * (PF & 1) + k / S) & 1u, acc_par = (pass * (PA & 1) + k / NA) & 1u;
+          const uint32_t full_par_n = (pn * (PF & 1) + kn / S) & 1u, acc_par_n = (pn * (PA & 1) + kn / NA) & 1u;
+          if (it + k >= n) break;
           if (!__all_sync(0xFFFFFFFFu, ready))
-            ok = warp_wait2(full_bar(r.i), r.parity, acc_empty(u.i), u.parity ^ 1u, kMmaTries);
+            ok = warp_wait2(full_bar(s), full_par, acc_empty(d), acc_par ^ 1u, kMmaTries);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(r.i) * (Cfg::kStageBytes / 16));
-          RingPos<S> rn = r;
-          RingPos<NA> un = u;
-          rn.next();
-          un.next();
-          ready = mbar_test2(full_bar(rn.i), rn.parity, acc_empty(un.i), un.parity ^ 1u);
+          ready = mbar_test2(full_bar(sn), full_par_n, acc_empty(dn), acc_par_n ^ 1u);
+          // (opaque, so that the sums below are not all worked out ahead and kept in registers)
+          uint64_t da = da0, db = db0;
+          asm volatile("" : "+l"(da), "+l"(db));
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < Cfg::kBK / 32; ++kk)   // 32 bytes along K: 2 in the descriptors' units
-              gemm_fp8_mma<C>(tmem_base + u.i * BN, da0 + off + 2 * kk, db0 + off + 2 * kk, Cfg::kIdesc,
-                              kk != 0 ? 1u : 0u);
-            gemm_fp8_commit<C>(empty_bar(r.i));
-            gemm_fp8_commit<C>(acc_full(u.i));
+              gemm_fp8_mma<C>(tmem_base + d * BN, da + s * (Cfg::kStageBytes / 16) + 2 * kk,
+                              db + s * (Cfg::kStageBytes / 16) + 2 * kk, Cfg::kIdesc, kk != 0 ? 1u : 0u);
+            gemm_fp8_commit<C>(empty_bar(s));
+            gemm_fp8_commit<C>(acc_full(d));
           }
           __syncwarp();
-          last = 1u | static_cast<uint32_t>(u.i) << 1 | u.parity << 8;
-          r = rn;
-          u = un;
         }
       }
-      // the last commits must have landed before TMEM is freed
-      if (last) mbar_wait_bounded(acc_full((last >> 1) & 0x7F), last >> 8);
+      // the last commits must have landed before TMEM is freed (one that never came was waited for)
+      if (ok && n > 0) mbar_wait_bounded(acc_full(static_cast<int>((n - 1) % NA)), static_cast<uint32_t>((n - 1) / NA & 1));
     }
   } else if (warp >= Cfg::kAddWarp0) {
     // ---------------- adding warps: TMEM lane quarter warp % 4, column half (warp - 4) / 4
