@@ -1,15 +1,19 @@
-// 8-bit GEMM with a scale per block of 128, on the 5th-generation tensor cores (tcgen05
-// kind::f8f6f4):
+// 8-bit GEMM with a scale per block of 128, on the 5th-generation tensor cores (tcgen05):
 //   D[m][n] = sum over K-blocks j of  sa[m][j] sb[n / 128][j] * (sum over k in block j of qa[m][k] qb[n][k]),
 // with A's codes [M][K] and scales [M][ceil(K/128)] as fp4q_quantize_fp8 or fp4q_add_rmsnorm_fp8
 // write them, and B's codes [N][K] and scales [ceil(N/128)][ceil(K/128)] from fp4q_quantize_fp8 with
-// tiles.  The sum inside a block is the tensor core's (fp32, in tensor memory); the sum over the
-// blocks is taken in fp32 registers, each block's sum times its two scales by one fused
-// multiply-add, and rounded once, to D's type.
+// tiles.
 //
-// Two kernels, both with one TMA producer warp, one MMA warp and warps that add up the blocks; the
-// codes travel through a ring of 128-byte-swizzled stages of one K-block, and two accumulators in
-// tensor memory let a block's MMAs run while the block before it is added.  Every wait is bounded.
+// Three kernels:
+//   gemm_fp8_kernel      many rows, any scales.  The tensor core sums inside a block (kind::f8f6f4, fp32
+//                        in tensor memory); the sum over the blocks is taken in fp32 registers, each
+//                        block's sum times its two scales by one fused multiply-add;
+//   gemm_fp8_mx_kernel   many rows, scales in powers of two.  The tensor core applies the scales
+//                        (kind::mxf8f6f4) and sums over all of K;
+//   gemm_fp8_few_kernel  few rows: B is the row operand, and K is split over a cluster.
+// D is rounded once, to its type.  All three have a TMA producer warp and an MMA warp; the codes travel
+// through a ring of 128-byte-swizzled stages of one K-block, and several accumulators in tensor memory
+// let MMAs run while what they left before is read.  Every wait is bounded.
 #pragma once
 
 #include <cuda.h>
@@ -205,8 +209,16 @@ __device__ __forceinline__ void lds_pairs(uint32_t addr, f32x2& a, f32x2& b) {
 // columns: its multiplier is one number a block, sa[row][j] * sb[n / 128][j], and a block costs it
 // one fused multiply-add per element.  Persistent, round-robin over the tiles.  C = 2 pairs the CTAs
 // of a cluster on one tile (cta_group::2, M = 256): each loads its 128 rows of A and half of B's, and
-// the leader issues the MMAs of both.
-// Tile t's row and column of tiles: down kGroup rows, then the next column, so that the tiles worked on
+// the leader issues the MMAs of both; that halves what B costs L2 and shared memory (8192^3: 593 us
+// against 627 us with one CTA to a 128 x 256 tile, when it was taken up).
+//
+// What bounds it, measured at 8192^3: the MMAs and copies alone take 440 us (at a clock the power cap
+// holds near 1.3 GHz), with the adding 522 us.  A block's turn through one of the two accumulators is MMAs
+// (600 cycles with their start), commit and wake-up (290), the adding warps' read (500 - 590, in steps of
+// 8 columns: 16, 32 or 64 at a time take 619, 755 and 598 us) and the arrival that frees it (300); more
+// accumulators of narrower tiles cost more in operand traffic than they hide (256 x 128: 613 us).
+
+// Tile t's row and column of tiles: down kTileGroup rows, then the next column, so that the tiles worked on
 // at one time (74 pairs: 16 rows by 4.6 columns) share their rows of A and of B in L2.  8192^3 takes
 // 523 us with fp32 scales and 397 us with E8M0, against 555 and 440 us down all 32 rows; groups of 8 and
 // 32 rows lie between, and where A's rows are few there is no difference.
@@ -583,6 +595,10 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 // the next.  The scales reach tensor memory without a copy instruction, which would wait its turn with
 // the MMAs: four warps, one per lane quarter, load four blocks' bytes of a row as one word and store it
 // (row r of the tile: lane r mod 32 of every quarter, column r / 32, byte j mod 4).
+//
+// Measured: 8192^3 in 397 us, 2.77 PFLOP/s, where adding in registers takes 570 us; 4096 x 8192 x 8192
+// keeps the tensor pipe 88 % busy (57 % when added in registers).  What bounds it is the power cap, and
+// below that the MMAs.
 template <int OT>
 struct GemmFp8MxConfig {
   static constexpr int kCtas = 2, kBM = 256, kBN = 224, kBK = kFp8Block;
@@ -792,6 +808,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 // One CTA to an SM and one tile to a CTA; where there are fewer tiles than SMs, the blocks of K are
 // split over a cluster.  A CTA's sums then go to the CTA of the cluster that owns their token (pushed
 // into its shared memory), which adds them in the order of their ranks: no atomics, no workspace.
+//
+// Measured: 1 x 14336 x 4096 in 12.7 us, of which B's 58.7 MB stream in 8.3 us (7.1 TB/s); the rest is the
+// first load (1.7 us), the sums and stores (0.6 us) and the gap to the next launch.  16 x 4096 x 14336 with
+// K over 1 / 2 / 3 / 4 CTAs: 29.4 / 17.1 / 14.1 / 13.7 us.  With two smaller CTAs to an SM the early start
+// of the next launch put two CTAs of one grid on an SM beside idle ones (64 x 14336 x 4096: 26.6 us
+// against 14.9).
 template <int BT_, int OT, int SF>
 struct GemmFp8FewConfig {
   static constexpr int kBT = BT_, kBK = kFp8Block;
