@@ -128,7 +128,7 @@ __device__ __forceinline__ void store_one(void* d, int64_t i, float v) {
     static_cast<uint16_t*>(d)[i] = static_cast<uint16_t>(pair_from_f32<kDtFp16>(v, 0.0f) & 0xFFFFu);
 }
 
-// Sixteen / eight neighbouring columns of one row of D, as far as they exist.
+// Eight neighbouring columns of one row of D, as far as they exist.
 template <int OT, int N>
 __device__ __forceinline__ void store_row_tail(const GemmFp8Args& g, int64_t row, int64_t col, const f32x2* acc) {
 #pragma unroll
@@ -157,19 +157,73 @@ __device__ __forceinline__ void store_row8(const GemmFp8Args& g, int64_t row, in
            pair_from_f32<OT>(acc[2]), pair_from_f32<OT>(acc[3]));
   }
 }
+// Sixteen columns of one row where rows keep a 16-byte alignment, so that a row ends between stores.
 template <int OT>
 __device__ __forceinline__ void store_row16(const GemmFp8Args& g, int64_t row, int64_t col, const f32x2* acc) {
-  if (g.vec == 0 || col + 16 > g.N) {
-    store_row_tail<OT, 16>(g, row, col, acc);
-  } else if (OT != kDtF32 && g.vec == 2) {
+  if (OT != kDtF32 && g.vec == 2) {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = pair_from_f32<OT == kDtF32 ? kDtBf16 : OT>(acc[i]);
     stg256(static_cast<uint16_t*>(g.d) + row * g.N + col, w);   // whole 32-byte sectors
+  } else if constexpr (OT == kDtF32) {
+    float* p = static_cast<float*>(g.d) + row * g.N + col;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float v[4];
+      f2_unpack(acc[i], v[0], v[1]);
+      f2_unpack(acc[i + 1], v[2], v[3]);
+      if (col + 2 * i < g.N)
+        stg128(p + 2 * i, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    }
   } else {
-    store_row8<OT>(g, row, col, acc);
-    store_row8<OT>(g, row, col + 8, acc + 4);
+    uint16_t* p = static_cast<uint16_t*>(g.d) + row * g.N + col;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4)
+      if (col + 2 * i < g.N)
+        stg128(p + 2 * i, pair_from_f32<OT>(acc[i]), pair_from_f32<OT>(acc[i + 1]), pair_from_f32<OT>(acc[i + 2]),
+               pair_from_f32<OT>(acc[i + 3]));
   }
+}
+// Sixteen columns of a warp's 32 rows (lane: row) where rows keep no such alignment: by way of shared
+// memory (`buf`, kUnalignedBytes of the warp's own), so that neighbouring lanes store neighbouring
+// columns.  With a lane to a row, every store of 2 bytes would touch a sector of its own.
+// Measured, bf16, a lane to a row and this way: 793 x 11180 x 6784 197 and 96 us (256 x 256 tiles), 175 and
+// 81 us (E8M0); N = 11181, stores of single elements, 197 and 107 us, 175 and 86 us; N = 11184, rows of 16-byte
+// alignment, 82 and 75 us.  UNROLL: 16 where 64 sums a thread leave the registers for it (104 -> 101 us with
+// 128 x 128 tiles), else 4.  All lanes take part.
+constexpr int kUnalignedPitch = 17, kUnalignedBytes = 32 * kUnalignedPitch * 4;
+template <int OT, int UNROLL>
+__device__ __forceinline__ void store_unaligned16(const GemmFp8Args& g, int64_t row0, int64_t col, const f32x2* acc,
+                                                  uint32_t buf, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float lo, hi;
+    f2_unpack(acc[i], lo, hi);
+    sts32(buf + 4u * (lane * kUnalignedPitch + 2 * i), __float_as_uint(lo));
+    sts32(buf + 4u * (lane * kUnalignedPitch + 2 * i + 1), __float_as_uint(hi));
+  }
+  __syncwarp();
+  if (OT != kDtF32 && (g.N & 1) == 0) {
+    // pairs of columns (D starts on 16 bytes, so a pair on 4), four rows at a time
+    const int c = 2 * (lane & 7);
+#pragma unroll UNROLL
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const uint32_t at = buf + 4u * (r * kUnalignedPitch + c);
+      if (row0 + r < g.M && col + c < g.N)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.d) + (row0 + r) * g.N + col + c) =
+            pair_from_f32<OT == kDtF32 ? kDtBf16 : OT>(__uint_as_float(lds32(at)), __uint_as_float(lds32(at + 4u)));
+    }
+  } else {
+    const int c = lane & 15;
+#pragma unroll UNROLL
+    for (int i = 0; i < 16; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      if (row0 + r < g.M && col + c < g.N)
+        store_one<OT>(g.d, (row0 + r) * g.N + col + c, __uint_as_float(lds32(buf + 4u * (r * kUnalignedPitch + c))));
+    }
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -232,20 +286,24 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8Args& g, int t, int& 
 
 constexpr int kMmaTries = 64;   // times an MMA warp asks for its barriers before it suspends
 
-template <int CTAS, int BN_, int OT, int SF>
+// ALIGNED: D's rows keep a 16-byte alignment.  A parameter: with both kinds of stores in one
+// kernel it took 5 % longer at 8192^3 (525 -> 553 us).
+template <int CTAS, int BN_, int OT, int SF, bool ALIGNED>
 struct GemmFp8Config {
   static constexpr int kCtas = CTAS;
   static constexpr int kBM = 128 * CTAS, kBN = BN_, kBK = kFp8Block;
   static constexpr int kOut = OT, kSf = SF;
+  static constexpr bool kAligned = ALIGNED;
   static constexpr int kARows = 128, kBRows = kBN / CTAS;   // a CTA's share of a stage
   static constexpr int kABytes = kARows * kBK, kBBytes = kBRows * kBK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = (196 * 1024) / kStageBytes;
   static constexpr int kBarOffset = kStages * kStageBytes;
-  static constexpr int kSmemBytes = 1024 + kBarOffset + 256;
   static constexpr int kAccs = 512 / kBN;                   // accumulators in tensor memory
   static constexpr int kTmemCols = kAccs * kBN;
   static constexpr int kAddWarp0 = 4, kAddWarps = 8;        // two per TMEM lane quarter
+  static constexpr int kBufOffset = kBarOffset + 256;       // rows of no alignment: a piece per adding warp
+  static constexpr int kSmemBytes = 1024 + kBufOffset + (ALIGNED ? 0 : kAddWarps * kUnalignedBytes);
   static constexpr int kCols = kBN / 2;                     // columns per adding warp
   static constexpr int kThreads = 32 * (kAddWarp0 + kAddWarps);
   // 128 sums a thread need more registers than 384 threads share out evenly (168): the first four
@@ -564,10 +622,18 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
           u.next();
         }
       }
-      if (ok && row < g.M) {
+      if constexpr (Cfg::kAligned) {
+        if (ok && row < g.M) {
+#pragma unroll
+          for (int c = 0; c < NC / 16; ++c)
+            if (col0 + 16 * c < g.N) store_row16<Cfg::kOut>(g, row, col0 + 16 * c, acc + 8 * c);
+        }
+      } else if (ok) {
+        const uint32_t buf = stage0 + Cfg::kBufOffset + (warp - Cfg::kAddWarp0) * kUnalignedBytes;
 #pragma unroll
         for (int c = 0; c < NC / 16; ++c)
-          if (col0 + 16 * c < g.N) store_row16<Cfg::kOut>(g, row, col0 + 16 * c, acc + 8 * c);
+          if (col0 + 16 * c < g.N)
+            store_unaligned16<Cfg::kOut, NC == 64 ? 16 : 4>(g, row - lane, col0 + 16 * c, acc + 8 * c, buf, lane);
       }
     }
   }
@@ -599,22 +665,24 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 // Measured: 8192^3 in 397 us, 2.77 PFLOP/s, where adding in registers takes 570 us; 4096 x 8192 x 8192
 // keeps the tensor pipe 88 % busy (57 % when added in registers).  What bounds it is the power cap, and
 // below that the MMAs.
-template <int OT>
+template <int OT, bool ALIGNED>
 struct GemmFp8MxConfig {
   static constexpr int kCtas = 2, kBM = 256, kBN = 224, kBK = kFp8Block;
   static constexpr int kOut = OT;
+  static constexpr bool kAligned = ALIGNED;                 // as in GemmFp8Config
   static constexpr int kARows = 128, kBRows = kBN / 2;      // a CTA's share of a stage
   static constexpr int kABytes = kARows * kBK, kBBytes = kBRows * kBK;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static_assert(kStageBytes % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms");
   static constexpr int kStages = (196 * 1024) / kStageBytes;
   static constexpr int kBarOffset = kStages * kStageBytes;
-  static constexpr int kSmemBytes = 1024 + kBarOffset + 256;
+  static constexpr int kBufOffset = kBarOffset + 256;
   static constexpr int kSfCols = 4 + 8;                     // A's 128 rows, B's 224 in 32-row cells
   static constexpr int kSfCol0 = 2 * kBN;
   static constexpr int kTmemCols = 512;
   static_assert(kSfCol0 + 2 * kSfCols <= kTmemCols);
   static constexpr int kSfWarp0 = 4, kEpiWarp0 = 8, kEpiWarps = 8;
+  static constexpr int kSmemBytes = 1024 + kBufOffset + (ALIGNED ? 0 : kEpiWarps * kUnalignedBytes);
   static constexpr int kCols = kBN / 2;                     // columns per epilogue warp
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
   // as gemm_fp8_idesc, with E8M0 scales (bit 23)
@@ -747,7 +815,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
       for (int c = 0; c < NC / 16; ++c) {
         f32x2 p[8];
         tmem_ld_pairs(src + 16 * c, p);
-        if (row < g.M && col0 + 16 * c < g.N) store_row16<Cfg::kOut>(g, row, col0 + 16 * c, p);
+        if constexpr (Cfg::kAligned) {
+          if (row < g.M && col0 + 16 * c < g.N) store_row16<Cfg::kOut>(g, row, col0 + 16 * c, p);
+        } else if (col0 + 16 * c < g.N) {
+          const uint32_t buf = stage0 + Cfg::kBufOffset + (warp - Cfg::kEpiWarp0) * kUnalignedBytes;
+          store_unaligned16<Cfg::kOut, 4>(g, row - lane, col0 + 16 * c, p, buf, lane);
+        }
       }
       tc_fence_before();
       __syncwarp();

@@ -79,9 +79,9 @@ fp4q_status check_registers(Kernel kernel) {
   return FP4Q_OK;
 }
 
-template <int CTAS, int BN, int OT, int SF>
+template <int CTAS, int BN, int OT, int SF, bool ALIGNED>
 fp4q_status launch_add(const Problem& p) {
-  using Cfg = GemmFp8Config<CTAS, BN, OT, SF>;
+  using Cfg = GemmFp8Config<CTAS, BN, OT, SF, ALIGNED>;
   fp4q_status st = check_registers<Cfg>(gemm_fp8_kernel<Cfg>);
   return st == FP4Q_OK ? launch_many<Cfg>(gemm_fp8_kernel<Cfg>, p) : st;
 }
@@ -146,6 +146,19 @@ Estimate estimate(const Variant& v, const GemmFp8Args& g, int sms, bool may_spli
           static_cast<int>(split)};
 }
 
+template <int OT, int SF, bool ALIGNED>
+fp4q_status launch_tiles(const Problem& p, int64_t one, int64_t pair, int64_t wide) {
+  if (wide <= one && wide <= pair) {
+    if constexpr (SF == kSfE8m0) {
+      using Cfg = GemmFp8MxConfig<OT, ALIGNED>;
+      return launch_many<Cfg>(gemm_fp8_mx_kernel<Cfg>, p);
+    } else {
+      return launch_add<2, 256, OT, SF, ALIGNED>(p);
+    }
+  }
+  return pair < one ? launch_add<2, 128, OT, SF, ALIGNED>(p) : launch_add<1, 128, OT, SF, ALIGNED>(p);
+}
+
 template <int OT, int SF>
 fp4q_status dispatch(const Problem& p) {
   int dev = 0, sms = 0;
@@ -161,13 +174,7 @@ fp4q_status dispatch(const Problem& p) {
     if (g.M <= 32) return launch_few<GemmFp8FewConfig<32, OT, SF>>(p, few.split);
     return launch_few<GemmFp8FewConfig<64, OT, SF>>(p, few.split);
   }
-  if (wide <= one && wide <= pair) {
-    if constexpr (SF == kSfE8m0)
-      return launch_many<GemmFp8MxConfig<OT>>(gemm_fp8_mx_kernel<GemmFp8MxConfig<OT>>, p);
-    else
-      return launch_add<2, 256, OT, SF>(p);
-  }
-  return pair < one ? launch_add<2, 128, OT, SF>(p) : launch_add<1, 128, OT, SF>(p);
+  return g.vec != 0 ? launch_tiles<OT, SF, true>(p, one, pair, wide) : launch_tiles<OT, SF, false>(p, one, pair, wide);
 }
 
 template <int OT>

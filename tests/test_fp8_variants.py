@@ -109,6 +109,35 @@ def test_arrays_at_the_least_alignment(F):
             assert torch.all(raw[:16] == 0xA5) and torch.all(raw[16 + M * N * 2:] == 0xA5)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, F32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("fmt", [o.F32, o.E8M0], ids=["f32", "e8m0"])
+@pytest.mark.parametrize("M,N,K", [(5, 1301, 272), (150, 1299, 784), (150, 1302, 784), (333, 4102, 1040),
+                                   (333, 4109, 1040), (640, 12001, 272), (1025, 4358, 400), (3000, 3099, 656),
+                                   (2049, 6, 272), (700, 1, 528)])
+def test_rows_of_no_alignment_are_exact(F, M, N, K, fmt, dtype):
+    """N that leaves D's rows without 16-byte alignment, odd and even, on the kernels for few, some and many
+    rows.  Small integers and scales of one, so that every sum is exact in fp32 and each output is its one
+    rounding; what lies around D stays."""
+    g = torch.Generator(device="cuda").manual_seed(N)
+    kb = -(-K // 128)
+    a = torch.randint(-2, 3, (M, K), generator=g, device="cuda").float()
+    b = torch.randint(-2, 3, (N, K), generator=g, device="cuda").float()
+    ref = (a.double() @ b.double().T).to(dtype)
+    ac, bc = a.to(torch.float8_e4m3fn), b.to(torch.float8_e4m3fn)
+    if fmt == o.F32:
+        sa, sb = (torch.ones((r, kb), device="cuda") for r in (M, -(-N // 128)))
+    else:
+        sa, sb = (torch.full((r, kb), 127, dtype=torch.uint8, device="cuda") for r in (M, -(-N // 128)))
+    size = ref.element_size()
+    code = {BF16: F.FP4Q_DTYPE_BF16, FP16: F.FP4Q_DTYPE_FP16, F32: F.FP4Q_DTYPE_F32}[dtype]
+    raw = torch.full((M * N * size + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    F.fp4q_gemm_fp8(fmt, code, ac, sa, bc, sb, M, N, K, raw.data_ptr() + 16)
+    synced(F)
+    end = 16 + M * N * size
+    assert torch.equal(raw[16:end].view(dtype).view(M, N), ref)
+    assert torch.all(raw[:16] == 0xA5) and torch.all(raw[end:] == 0xA5)
+
+
 def test_quantize_past_32_bit_offsets(F):
     """More than 2^32 bytes of input and 2^31 of codes: rows from the start, around the borders and the end."""
     M, K = 140000, 16384
