@@ -241,9 +241,10 @@ __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_tiles_kernel(Fp
 // its one write: C chunks of 16 channels a thread.  C = 2 where there are many rows (smaller CTAs, more
 // of them on an SM in different phases: 16384 x 8192 bf16 takes 146 us, 6.4 TB/s, against 156 us with
 // C = 1 and 182 us with C = 4); C = 1 where a row has an SM to itself and its latency counts (1 x 4096:
-// 2.3 us against 3.0).  h, the square sum (per thread in order, then over
-// lanes and warps) and y stay in fp32: y is rounded once, to its code, and the norm is of h as it was
-// before it is rounded to be stored.
+// 2.3 us against 3.0).  h, the square sum and y stay in fp32: y is rounded once, to its code, and the
+// norm is of h as it was before it is rounded to be stored.  The square sum goes over a chunk, then over
+// groups of 32 chunks, then over the groups: one order for both values of C, so that a row's result does not
+// depend on the batch it is in.
 struct Fp8NormArgs {
   const uint16_t* x;
   const uint16_t* residual;   // or null
@@ -260,14 +261,15 @@ constexpr int kFp8NormThreads = 1024;   // at most; K / (16 C) rounded up to who
 
 template <int DT, int SF, int C, bool RES>
 __global__ void __launch_bounds__(kFp8NormThreads) add_rmsnorm_fp8_kernel(Fp8NormArgs a) {
-  __shared__ float s_part[2][kFp8NormThreads / 32];
+  constexpr int kGroups = 2 * kFp8NormThreads / 32;   // groups of 32 chunks in the longest row
+  __shared__ float s_part[2][kGroups];
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x, n_warps = T >> 5;
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, parity ^= 1) {
     f32x2 h[C][8];
-    float ss = 0.0f;
+    float ss[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = (tid + c * T) * kFp8Chunk;
@@ -295,13 +297,20 @@ __global__ void __launch_bounds__(kFp8NormThreads) add_rmsnorm_fp8_kernel(Fp8Nor
       for (int i = 0; i < 8; ++i) sq = f2_fma(h[c][i], h[c][i], sq);
       float s0, s1;
       f2_unpack(sq, s0, s1);
-      ss += s0 + s1;
+      ss[c] = s0 + s1;
     }
+    // group g holds chunks 32 g ... 32 g + 31, whatever C is
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-    if (lane == 0) s_part[parity][warp] = ss;
+    for (int d = 16; d > 0; d /= 2)
+#pragma unroll
+      for (int c = 0; c < C; ++c) ss[c] += __shfl_xor_sync(0xFFFFFFFFu, ss[c], d);
+    if (lane == 0)
+#pragma unroll
+      for (int c = 0; c < C; ++c) s_part[parity][warp + c * n_warps] = ss[c];
     __syncthreads();   // the other half of s_part is written only after every thread passed this
-    float tot = lane < n_warps ? s_part[parity][lane] : 0.0f;
+    const int n_groups = C * n_warps;
+    float tot = lane < n_groups ? s_part[parity][lane] : 0.0f;
+    tot += lane + 32 < n_groups ? s_part[parity][lane + 32] : 0.0f;
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) tot += __shfl_xor_sync(0xFFFFFFFFu, tot, d);
     const float rstd = __frsqrt_rn(__fdiv_rn(tot, static_cast<float>(a.K)) + a.eps);

@@ -138,6 +138,23 @@ def test_rows_of_no_alignment_are_exact(F, M, N, K, fmt, dtype):
     assert torch.all(raw[:16] == 0xA5) and torch.all(raw[end:] == 0xA5)
 
 
+@pytest.mark.parametrize("residual", [False, True], ids=["alone", "residual"])
+@pytest.mark.parametrize("K", [16, 528, 4096, 5008, 8192, 14336, 16384, 16400, 32768])
+def test_norm_of_a_row_is_the_same_in_any_batch(F, K, residual):
+    """One token, a few and more than there are SMs: the square sum of a row keeps its order, to the bit."""
+    M = 700
+    x, r = activations(M, K, K), activations(M, K, K + 1)
+    w = activations(1, K, K + 2)[0]
+    ref = F.add_rmsnorm_fp8(x, r if residual else None, w, 1e-6)
+    for lo, hi in ((0, 1), (3, 20), (40, 188), (100, 249), (699, 700)):
+        part = F.add_rmsnorm_fp8(x[lo:hi], r[lo:hi] if residual else None, w, 1e-6)
+        synced(F)
+        assert torch.equal(part[1], ref[1][lo:hi])
+        assert torch.equal(part[0].view(torch.uint8), ref[0][lo:hi].view(torch.uint8))
+        if residual:
+            assert torch.equal(part[2], ref[2][lo:hi])
+
+
 def test_quantize_past_32_bit_offsets(F):
     """More than 2^32 bytes of input and 2^31 of codes: rows from the start, around the borders and the end."""
     M, K = 140000, 16384
