@@ -266,7 +266,7 @@ fp4q_status fp4q_gemm(int format, const void* a_codes, const void* a_scales, con
  * These calls own nothing and allocate nothing; calls on different streams are independent.  Every
  * array belongs to the CUDA context that is current, as the stream does.  An output that overlaps
  * an input or another output is refused with FP4Q_ERR_ARG, but for the two cases fp4q_add_rmsnorm_fp8
- * names. */
+ * names; an array reaches from its first to its last byte, the gaps between its rows included. */
 typedef enum { FP4Q_FP8_SCALE_F32 = 0, FP4Q_FP8_SCALE_E8M0 = 1 } fp4q_fp8_scale;
 typedef enum { FP4Q_DTYPE_BF16 = 0, FP4Q_DTYPE_FP16 = 1, FP4Q_DTYPE_F32 = 2 } fp4q_dtype;
 
@@ -285,8 +285,9 @@ fp4q_status fp4q_quantize_fp8(int scale_format, int dtype, int block_rows, const
  * of 8), 16-byte aligned; weight: dtype [K], 16-byte aligned.  residual and residual_out are both given
  * or both NULL (ldr and ldo are then ignored).  residual_out may be residual itself (with ldo = ldr) or
  * x itself (with ldo = ldx).  eps: finite, >= 0.  K at most 32768; the rest as for fp4q_quantize_fp8.
- * The sum of squares is fp32, in a fixed order: the result of a row depends on that row and K alone.
- * Rows whose sum of squares passes fp32's range give zeros, as 1 / sqrt(inf) does. */
+ * The sum of squares is fp32, in a fixed order: the result of a row depends on that row, weight, eps and
+ * K alone.  Rows whose sum of squares passes fp32's range give zeros, as 1 / sqrt(inf) does; a row of zeros
+ * with eps = 0 gives NaN. */
 fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int64_t ldx, const void* residual,
                                  int64_t ldr, const void* weight, float eps, int64_t M, int64_t K,
                                  void* residual_out, int64_t ldo, void* codes_out, void* scales_out, void* stream);
@@ -295,11 +296,13 @@ fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int
  *   D[m][n] = sum_j a_scales[m][j] * b_scales[n / 128][j] * sum_{k in block j} a_codes[m][k] b_codes[n][k],
  * A [M][K] an activation's codes and scales (block_rows 1, or fp4q_add_rmsnorm_fp8's), B [N][K] a
  * weight's (block_rows 128), both of scale_format.  d: out_dtype (FP4Q_DTYPE_BF16, _FP16 or _F32) [M][N],
- * row-major and contiguous, 16-byte aligned.  Sums are fp32: a block's on the tensor core
- * (tcgen05 kind::f8f6f4), the blocks' in registers; D is rounded once.  Any scale bytes and codes are
+ * row-major and contiguous, 16-byte aligned.  Sums are fp32: a block's on the tensor core,
+ * the blocks' in registers, over parts of K first where there are few rows (tcgen05 kind::f8f6f4); with
+ * E8M0 scales and many rows all on the tensor core (kind::mxf8f6f4).  D is rounded once.  Any scale bytes and codes are
  * taken, NaN ones too.  M, N >= 0 and K a positive multiple of 16 (an empty M or N launches nothing),
  * each below 2^31 - 512, their pairwise products at most 2^40.  Codes 16-byte aligned, scales as in
- * fp4q_quantize_fp8.  Deterministic. */
+ * fp4q_quantize_fp8.  The same call on the same device gives the same bits; the order in which blocks are
+ * added, and so the last bits, may differ with M and N and from device to device. */
 fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
                           const void* b_codes, const void* b_scales, int64_t M, int64_t N, int64_t K, void* d,
                           void* stream);

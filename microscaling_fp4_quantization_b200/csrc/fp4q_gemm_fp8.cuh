@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 // (row r of the tile: lane r mod 32 of every quarter, column r / 32, byte j mod 4).
 //
 // Measured: 8192^3 in 397 us, 2.77 PFLOP/s, where adding in registers takes 570 us; 4096 x 8192 x 8192
-// keeps the tensor pipe 88 % busy (57 % when added in registers).  What bounds it is the power cap, and
+// keeps the tensor pipe 85 to 88 % busy (57 % when added in registers).  What bounds it is the power cap, and
 // below that the MMAs.
 template <int OT, bool ALIGNED>
 struct GemmFp8MxConfig {

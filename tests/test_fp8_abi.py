@@ -53,6 +53,13 @@ def test_norm_refusals(F):
     assert n(M=0, x=None, w=None, codes=None, scales=None) == F.FP4Q_OK
 
 
+def test_arrays_between_each_others_rows_are_refused(F):
+    """An array reaches from its first to its last byte: one in the gaps between another's rows overlaps it."""
+    assert F.raw_call("fp4q_add_rmsnorm_fp8", 0, 0, A, 512, FAR[0], 256, FAR[1], 1e-6, 4, 256, A + 512, 512, FAR[3],
+                      FAR[4], None) == F.FP4Q_ERR_ARG
+    assert F.raw_call("fp4q_quantize_fp8", 0, 0, 1, A, 1024, 2, 256, A + 512, FAR[1], None) == F.FP4Q_ERR_ARG
+
+
 def test_gemm_refusals(F):
     def g(fmt=0, dt=0, ac=A, sa=FAR[0], bc=FAR[1], sb=FAR[2], M=4, N=130, K=256, d=FAR[3]):
         return F.raw_call("fp4q_gemm_fp8", fmt, dt, ac, sa, bc, sb, M, N, K, d, None)

@@ -155,6 +155,19 @@ def test_norm_of_a_row_is_the_same_in_any_batch(F, K, residual):
             assert torch.equal(part[2], ref[2][lo:hi])
 
 
+@pytest.mark.parametrize("fmt", [o.F32, o.E8M0], ids=["f32", "e8m0"])
+def test_norm_of_zeros_without_eps(F, fmt):
+    """0 / sqrt(0 + 0) is NaN throughout the row, and in that row alone."""
+    x = activations(3, 528, 1)
+    x[1] = 0
+    w = torch.ones(528, dtype=BF16, device="cuda")
+    codes, scales, _ = F.add_rmsnorm_fp8(x, None, w, 0.0, fmt)
+    synced(F)
+    c = np_codes(codes)
+    assert np.all(c[1] & 0x7F == 0x7F) and np.all(c[[0, 2]] & 0x7F != 0x7F)
+    assert torch.all(torch.isnan(scales.float()[1])) and not torch.any(torch.isnan(scales.float()[[0, 2]]))
+
+
 def test_quantize_past_32_bit_offsets(F):
     """More than 2^32 bytes of input and 2^31 of codes: rows from the start, around the borders and the end."""
     M, K = 140000, 16384
