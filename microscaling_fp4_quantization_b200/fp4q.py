@@ -8,6 +8,7 @@ ImportError when it is missing; there is no fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -94,6 +95,17 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _allocating_on(stream, device):
+    """A context in which torch allocates on `stream` (None: the current one), so that its allocator
+    reuses a call's outputs in the order of the stream that the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 class Plan:
@@ -246,6 +258,10 @@ def raw_call(name: str, *args) -> int:
 
 
 # ---------------------------------------------------------------- tensor conveniences
+#
+# `stream`: a torch.cuda.Stream or a stream's handle; None is the current stream.  A call's outputs are
+# allocated on the stream it runs on.  An input that lives on another stream is the caller's to order
+# before the call, and to keep (or to record with Tensor.record_stream) until the call's stream has read it.
 
 def empty_outputs(plan: Plan, M: int, K: int, device="cuda"):
     """Allocate codes (uint8 [M, K/2]), scales (uint8 [M, K/g]) and the fp32 tensor scale."""
@@ -262,7 +278,8 @@ def rotate_quantize(plan: Plan, x, tensor_scale=None, stream=None) -> Tuple[obje
     if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D bf16 CUDA tensor")
     M, K = x.shape
-    codes, scales, ts = empty_outputs(plan, M, K, x.device)
+    with _allocating_on(stream, x.device):
+        codes, scales, ts = empty_outputs(plan, M, K, x.device)
     if tensor_scale is not None:
         ts = tensor_scale
     fp4q_rotate_quantize(plan, x, M, K, codes, scales, ts if plan.fmt == FP4Q_NVFP4 else None, stream)
@@ -332,13 +349,26 @@ def _fp8_array(name: str, t, shape, dtype, index):
     return t
 
 
+def _fp8_empty(shape, dtype, index, stream):
+    """An output of a call on `stream`."""
+    if stream is None:
+        return _torch.empty(shape, dtype=dtype, device=index)
+    _fp8_check_stream(stream, index)
+    with _allocating_on(stream, index):
+        return _torch.empty(shape, dtype=dtype, device=index)
+
+
+def _fp8_check_stream(stream, index) -> None:
+    if not isinstance(stream, int) and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on CUDA device {index}")
+
+
 def _fp8_call(name: str, index: int, stream, *args) -> None:
     """The C call `name` on the device's current stream, or on the given one, with the device current."""
     if stream is None:
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
-        if stream.device.index != index:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on CUDA device {index}")
+        _fp8_check_stream(stream, index)
         stream = stream.cuda_stream
     if _current_device() == index:
         status = getattr(_lib, name)(*args, stream)
@@ -365,9 +395,9 @@ def quantize_fp8(x, block_rows: int = 1, scale_format: int = FP4Q_FP8_SCALE_F32,
     M, K = shape
     ldx = K if x.is_contiguous() else _fp8_ld("x", x)
     s_shape = (-(-M // block_rows), -(-K // 128))
-    codes = _torch.empty(shape, dtype=_e4m3, device=x.device) if codes is None else \
+    codes = _fp8_empty(shape, _e4m3, index, stream) if codes is None else \
         _fp8_array("codes", codes, shape, _e4m3, index)
-    scales = _torch.empty(s_shape, dtype=s_dtype, device=x.device) if scales is None else \
+    scales = _fp8_empty(s_shape, s_dtype, index, stream) if scales is None else \
         _fp8_array("scales", scales, s_shape, s_dtype, index)
     _fp8_call("fp4q_quantize_fp8", index, stream, scale_format, dtype, block_rows, x.data_ptr(), ldx, M, K,
               codes.data_ptr(), scales.data_ptr())
@@ -396,16 +426,16 @@ def add_rmsnorm_fp8(x, residual, weight, eps: float, scale_format: int = FP4Q_FP
     if residual is not None:
         ldr = _fp8_like("residual", residual, shape, t_dtype, index)
         if residual_out is None:
-            residual_out = _torch.empty(shape, dtype=t_dtype, device=x.device)
+            residual_out = _fp8_empty(shape, t_dtype, index, stream)
         else:
             ldo = _fp8_like("residual_out", residual_out, shape, t_dtype, index)
         p_res, p_out = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out goes with a residual")
     s_shape = (M, -(-K // 128))
-    codes = _torch.empty(shape, dtype=_e4m3, device=x.device) if codes is None else \
+    codes = _fp8_empty(shape, _e4m3, index, stream) if codes is None else \
         _fp8_array("codes", codes, shape, _e4m3, index)
-    scales = _torch.empty(s_shape, dtype=s_dtype, device=x.device) if scales is None else \
+    scales = _fp8_empty(s_shape, s_dtype, index, stream) if scales is None else \
         _fp8_array("scales", scales, s_shape, s_dtype, index)
     if M > 0 and K > 0:   # (an empty tensor's null pointers say nothing about a residual)
         _fp8_call("fp4q_add_rmsnorm_fp8", index, stream, scale_format, dtype, x.data_ptr(), ldx, p_res, ldr,
@@ -437,7 +467,7 @@ def gemm_fp8(a_codes, a_scales, b_codes, b_scales, out_dtype=None, out=None, str
     dtype = _fp8_out_dtypes.get(out_dtype)
     if dtype is None:
         raise ValueError("out_dtype must be bf16, fp16 or fp32")
-    out = _torch.empty((M, N), dtype=out_dtype, device=a_codes.device) if out is None else \
+    out = _fp8_empty((M, N), out_dtype, index, stream) if out is None else \
         _fp8_array("out", out, (M, N), out_dtype, index)
     _fp8_call("fp4q_gemm_fp8", index, stream, fmt, dtype, a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
               b_scales.data_ptr(), M, N, K, out.data_ptr())
