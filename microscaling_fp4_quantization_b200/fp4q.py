@@ -292,12 +292,13 @@ def quant_error(plan: Plan, x, tensor_scale=None, stream=None):
     if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x must be a contiguous 2-D bf16 CUDA tensor")
     M, K = x.shape
-    out = torch.empty(3, dtype=torch.float64, device=x.device)
-    ts = tensor_scale
-    if plan.fmt == FP4Q_NVFP4 and ts is None:
-        ts = torch.empty(1, dtype=torch.float32, device=x.device)
-    fp4q_quant_error(plan, x, M, K, ts, out, stream)
-    s, e, q = out.tolist()
+    with _allocating_on(stream, x.device):   # the read back waits for that stream too
+        out = torch.empty(3, dtype=torch.float64, device=x.device)
+        ts = tensor_scale
+        if plan.fmt == FP4Q_NVFP4 and ts is None:
+            ts = torch.empty(1, dtype=torch.float32, device=x.device)
+        fp4q_quant_error(plan, x, M, K, ts, out, stream)
+        s, e, q = out.tolist()
     return s, e, q
 
 

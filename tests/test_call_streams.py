@@ -132,6 +132,26 @@ def test_calls_run_on_the_given_stream(F, operands, name, kind):
     assert all(same(a, b) for a, b in zip(got, want))
 
 
+@pytest.mark.parametrize("kind", ["object", "handle"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_error_pass_waits_for_the_given_stream(F, fmt, kind):
+    """The energies come back as numbers: they are read once the given stream has them."""
+    if fmt == "nvfp4":
+        plan = F.fp4q_plan_create(F.FP4Q_NVFP4, 16, 16, F.FP4Q_SCALE_NV_DYNAMIC)
+    else:
+        plan = F.fp4q_plan_create(F.FP4Q_MXFP4, 32, 32, F.FP4Q_SCALE_FLOOR_OCP)
+    new = values(M, H, 12)
+    want = F.quant_error(plan, new)
+    x = values(M, H, 11)
+    assert F.quant_error(plan, x) != want   # (and leaves other energies in the memory that is reused)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(DELAY)
+        x.copy_(new)
+    assert F.quant_error(plan, x, stream=handle_of(kind, side)) == want
+
+
 def test_a_stream_of_another_device_is_refused(F, operands):
     class Elsewhere:
         device, cuda_stream = torch.device("cuda", 1), 0
