@@ -298,8 +298,12 @@ fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int
  * weight's (block_rows 128), both of scale_format.  d: out_dtype (FP4Q_DTYPE_BF16, _FP16 or _F32) [M][N],
  * row-major and contiguous, 16-byte aligned.  Sums are fp32: a block's on the tensor core,
  * the blocks' in registers, over parts of K first where there are few rows (tcgen05 kind::f8f6f4); with
- * E8M0 scales and many rows all on the tensor core (kind::mxf8f6f4).  D is rounded once.  Any scale bytes and codes are
- * taken, NaN ones too.  M, N >= 0 and K a positive multiple of 16 (an empty M or N launches nothing),
+ * E8M0 scales and many rows all on the tensor core (kind::mxf8f6f4).  D is rounded once.  Any codes and scales are
+ * taken, NaN ones too (fp32 scales: negative and infinite ones too).  D is the formula's value where a block's
+ * two scales multiply to at least 2^-126 and less than 2^128 in magnitude.  Outside, the kernel decides: the
+ * product of the scales may be formed in fp32 first.  Below, the block's part of D is then off by at most 2^-150
+ * times the block's sum (2^-125 at most), as where a block of zeros meets any other.  From 2^128 on it is the formula's
+ * value, infinity, or NaN where the block's sum is 0.  M, N >= 0 and K a positive multiple of 16 (an empty M or N launches nothing),
  * each below 2^31 - 512, their pairwise products at most 2^40.  Codes 16-byte aligned, scales as in
  * fp4q_quantize_fp8.  The same call on the same device gives the same bits; the order in which blocks are
  * added, and so the last bits, may differ with M and N and from device to device. */
