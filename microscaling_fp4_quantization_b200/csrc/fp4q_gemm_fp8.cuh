@@ -108,8 +108,8 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 // until its block is added: converting it where it is loaded would wait for the load.
 template <int SF>
 __device__ __forceinline__ uint32_t load_scale(const void* scales, int64_t i) {
-  if constexpr (SF == kSfF32) return __ldg(static_cast<const uint32_t*>(scales) + i);
-  return __ldg(static_cast<const uint8_t*>(scales) + i);
+  if constexpr (SF == kSfF32) return ld_u32(static_cast<const uint32_t*>(scales) + i);
+  return ld_u8(static_cast<const uint8_t*>(scales) + i);
 }
 template <int SF>
 __device__ __forceinline__ float scale_value(uint32_t w) {
@@ -696,11 +696,11 @@ __device__ __forceinline__ uint32_t load_scale_word(const uint8_t* scales, int64
                                                     bool vec) {
   if (row >= rows) return 0u;
   const uint8_t* p = scales + row * kb + j;
-  if (vec) return __ldg(reinterpret_cast<const uint32_t*>(p));
+  if (vec) return ld_u32(p);
   uint32_t w = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (j + i < kb) w |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
+    if (j + i < kb) w |= ld_u8(p + i) << (8 * i);
   return w;
 }
 
