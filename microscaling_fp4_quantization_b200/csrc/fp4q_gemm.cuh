@@ -140,10 +140,10 @@ __device__ __forceinline__ uint4 stage_scale_words(const uint8_t* scales, int64_
   if (row >= rows) return make_uint4(0u, 0u, 0u, 0u);
   if constexpr (FMT == kNV) {
     // 16 scale bytes: 4 per MMA
-    return __ldg(reinterpret_cast<const uint4*>(scales + row * (K / 16) + static_cast<int64_t>(ks) * 16));
+    return ld_u128(scales + row * (K / 16) + static_cast<int64_t>(ks) * 16);
   } else {
     // 8 scale bytes: 2 per MMA; word q holds MMAs 2q (bytes 0-1) and 2q + 1 (bytes 2-3)
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(scales + row * (K / 32) + static_cast<int64_t>(ks) * 8));
+    const uint2 v = ld_u64(scales + row * (K / 32) + static_cast<int64_t>(ks) * 8);
     return make_uint4(v.x, v.y, 0u, 0u);
   }
 }

@@ -50,3 +50,36 @@ def test_8bit(F, M, N, fmt):
     assert F.fp4q_device_status() == F.FP4Q_OK
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("M,N", [(1, 2048), (130, 2048), (1100, 2048), (2500, 2080)])
+def test_fp4(F, M, N, fmt):
+    K = 1024
+    if fmt == "nvfp4":
+        code, plan = F.FP4Q_NVFP4, F.fp4q_plan_create(F.FP4Q_NVFP4, 16, 16, F.FP4Q_SCALE_NV_DYNAMIC)
+    else:
+        code, plan = F.FP4Q_MXFP4, F.fp4q_plan_create(F.FP4Q_MXFP4, 32, 32, F.FP4Q_SCALE_FLOOR_OCP)
+    b = F.rotate_quantize(plan, values(N, K, 1000))
+    xs = [values(M, K, i) for i in range(TURNS)]
+    want = []
+
+    def product(a, out):
+        F.fp4q_gemm(code, a[0], a[1], a[2], b[0], b[1], b[2], M, N, K, out)
+        return out
+
+    for x in xs:
+        a = F.rotate_quantize(plan, x)
+        torch.cuda.synchronize()
+        want.append(product(a, torch.empty((M, N), dtype=BF16, device="cuda")))
+        torch.cuda.synchronize()
+    a = F.empty_outputs(plan, M, K)
+    got = [torch.empty_like(want[0]) for _ in xs]
+    torch.cuda.synchronize()
+    for x, d in zip(xs, got):
+        F.fp4q_rotate_quantize(plan, x, M, K, a[0], a[1], a[2] if code == F.FP4Q_NVFP4 else None)
+        product(a, d)
+    torch.cuda.synchronize()
+    assert F.fp4q_device_status() == F.FP4Q_OK
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
