@@ -353,6 +353,14 @@ fp4q_status fp4q_device_status(void);
  * No fault, trap or unbounded wait is involved.  stream: as for the other calls. */
 fp4q_status fp4q_selftest_wait_timeout(void* stream);
 
+/* Which kernel fp4q_gemm_fp8 takes for these sizes on a device of sm_count SMs (0: the current device's
+ * count): the tile of D it works on, and the CTAs that K is split over.  Tiles of 16, 32 and 64 x 128 are the
+ * kernel for few rows, which splits less where clusters of that size are not all resident at once; tiles
+ * of 128 x 128, 256 x 128 and 256 x 256 add blocks in registers, those of 256 x 224 on the tensor core.  For tests
+ * that have to reach every kernel.  Launches nothing.  Sizes as for fp4q_gemm_fp8, none of them 0. */
+fp4q_status fp4q_selftest_gemm_fp8_choice(int scale_format, int64_t M, int64_t N, int64_t K, int sm_count, int* tile_m,
+                                          int* tile_n, int* split);
+
 /* Static string for a status code. */
 const char* fp4q_status_string(fp4q_status status);
 

@@ -456,6 +456,16 @@ fp4q_status check_fp8_rows(int64_t M, int64_t K, int64_t ld) {
   return FP4Q_OK;
 }
 
+// Shape rules of the 8-bit product.
+fp4q_status check_fp8_gemm(int64_t M, int64_t N, int64_t K) {
+  constexpr int64_t kMaxDim = (int64_t(1) << 31) - 512;   // 32-bit TMA coordinates, with a tile past the end
+  if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP4Q_ERR_SHAPE;
+  if (M == 0 || N == 0) return FP4Q_OK;
+  if (K == 0) return FP4Q_ERR_SHAPE;   // an empty reduction, as in fp4q_gemm
+  if (M > (int64_t(1) << 40) / K || N > (int64_t(1) << 40) / K || M > (int64_t(1) << 40) / N) return FP4Q_ERR_SHAPE;
+  return FP4Q_OK;
+}
+
 // No C++ exception crosses the ABI: the launchers keep tables that can run out of memory.
 template <class F>
 fp4q_status no_throw(F&& f) {
@@ -892,11 +902,9 @@ fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, 
   if (!valid_fp8_scale(scale_format) ||
       (out_dtype != FP4Q_DTYPE_BF16 && out_dtype != FP4Q_DTYPE_FP16 && out_dtype != FP4Q_DTYPE_F32))
     return FP4Q_ERR_UNSUPPORTED;
-  constexpr int64_t kMaxDim = (int64_t(1) << 31) - 512;   // 32-bit TMA coordinates, with a tile past the end
-  if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FP4Q_ERR_SHAPE;
+  fp4q_status st = check_fp8_gemm(M, N, K);
+  if (st != FP4Q_OK) return st;
   if (M == 0 || N == 0) return FP4Q_OK;
-  if (K == 0) return FP4Q_ERR_SHAPE;   // an empty reduction, as in fp4q_gemm
-  if (M > (int64_t(1) << 40) / K || N > (int64_t(1) << 40) / K || M > (int64_t(1) << 40) / N) return FP4Q_ERR_SHAPE;
   if (!a_codes || !a_scales || !b_codes || !b_scales || !d) return FP4Q_ERR_ARG;
   if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(d, 16) ||
       !aligned(a_scales, fp8_scale_align(scale_format)) || !aligned(b_scales, fp8_scale_align(scale_format)))
@@ -914,6 +922,16 @@ fp4q_status fp4q_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, 
 
 fp4q_status fp4q_selftest_wait_timeout(void* stream) {
   return launch_wait_timeout_selftest(static_cast<cudaStream_t>(stream));
+}
+
+fp4q_status fp4q_selftest_gemm_fp8_choice(int scale_format, int64_t M, int64_t N, int64_t K, int sm_count, int* tile_m,
+                                          int* tile_n, int* split) {
+  if (!valid_fp8_scale(scale_format)) return FP4Q_ERR_UNSUPPORTED;
+  if (!tile_m || !tile_n || !split || sm_count < 0 || sm_count == 1) return FP4Q_ERR_ARG;   // pairs take two SMs
+  fp4q_status st = check_fp8_gemm(M, N, K);
+  if (st != FP4Q_OK) return st;
+  if (M == 0 || N == 0) return FP4Q_ERR_SHAPE;
+  return gemm_fp8_choice(scale_format, M, N, K, sm_count, tile_m, tile_n, split);
 }
 
 fp4q_status fp4q_device_status(void) {

@@ -191,6 +191,9 @@ fp4q_status launch_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, i
 fp4q_status launch_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
                             const void* b_codes, const void* b_scales, int64_t M, int64_t N, int64_t K, void* d,
                             cudaStream_t stream);
+// The tile and the split of K that launch_gemm_fp8 chooses; sms 0: the current device's.
+fp4q_status gemm_fp8_choice(int scale_format, int64_t M, int64_t N, int64_t K, int sms, int* tile_m, int* tile_n,
+                            int* split);
 fp4q_status launch_tensor_scale_finalize(const float* partials, int n, float* out, cudaStream_t stream);
 fp4q_status launch_quant_error_empty(const double* partials, double* out, cudaStream_t stream);
 // Device address of the no-allocation path's fixed scratch (kNoAllocMaxPartials floats).

@@ -127,8 +127,10 @@ struct Variant {
 constexpr Variant kFew16{16, 128, 1, 250, 60, 36}, kFew32{32, 128, 1, 250, 110, 31}, kFew64{64, 128, 1, 170, 250, 31};
 // by scale format: with E8M0 the widest tile has its scales applied by the tensor core
 constexpr Variant kOne[2] = {{128, 128, 1, 300, 140, 32}, {128, 128, 1, 280, 140, 33}};
-constexpr Variant kPair[2] = {{256, 128, 2, 320, 130, 30}, {256, 128, 2, 340, 120, 34}};
 constexpr Variant kWide[2] = {{256, 256, 2, 430, 150, 48}, {256, 224, 2, 470, 90, 30}};
+// fp32 scales alone: with E8M0 a pair's rounds are as many as those of the 128 x 128 tiles or more, and one
+// of its neighbours is never slower
+constexpr Variant kPair{256, 128, 2, 320, 130, 30};
 
 struct Estimate {
   int64_t time;
@@ -146,9 +148,29 @@ Estimate estimate(const Variant& v, const GemmFp8Args& g, int sms, bool may_spli
           static_cast<int>(split)};
 }
 
+// The variant for a product, and the CTAs its K is split over.
+struct Choice {
+  const Variant* v;
+  int split;
+};
+Choice choose(int scale_format, const GemmFp8Args& g, int sms) {
+  const Variant* few = g.M <= 16 ? &kFew16 : g.M <= 32 ? &kFew32 : &kFew64;
+  const Estimate e = estimate(*few, g, sms, true);
+  Choice c{few, e.split};
+  int64_t best = e.time;
+  auto consider = [&](const Variant* v) {   // a tie goes to the one considered first
+    const int64_t t = estimate(*v, g, sms, false).time;
+    if (t < best) c = {v, 1}, best = t;
+  };
+  consider(&kWide[scale_format]);
+  consider(&kOne[scale_format]);
+  if (scale_format == FP4Q_FP8_SCALE_F32) consider(&kPair);
+  return c;
+}
+
 template <int OT, int SF, bool ALIGNED>
-fp4q_status launch_tiles(const Problem& p, int64_t one, int64_t pair, int64_t wide) {
-  if (wide <= one && wide <= pair) {
+fp4q_status launch_tiles(const Variant* v, const Problem& p) {
+  if (v == &kWide[SF]) {
     if constexpr (SF == kSfE8m0) {
       using Cfg = GemmFp8MxConfig<OT, ALIGNED>;
       return launch_many<Cfg>(gemm_fp8_mx_kernel<Cfg>, p);
@@ -156,25 +178,28 @@ fp4q_status launch_tiles(const Problem& p, int64_t one, int64_t pair, int64_t wi
       return launch_add<2, 256, OT, SF, ALIGNED>(p);
     }
   }
-  return pair < one ? launch_add<2, 128, OT, SF, ALIGNED>(p) : launch_add<1, 128, OT, SF, ALIGNED>(p);
+  if constexpr (SF == kSfF32)
+    if (v == &kPair) return launch_add<2, 128, OT, SF, ALIGNED>(p);
+  return launch_add<1, 128, OT, SF, ALIGNED>(p);
+}
+
+fp4q_status current_sms(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? FP4Q_OK : cuda_fail(e, "cudaDeviceGetAttribute");
 }
 
 template <int OT, int SF>
 fp4q_status dispatch(const Problem& p) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  const GemmFp8Args& g = p.g;
-  const Estimate few = estimate(g.M <= 16 ? kFew16 : g.M <= 32 ? kFew32 : kFew64, g, sms, true);
-  const int64_t one = estimate(kOne[SF], g, sms, false).time, pair = estimate(kPair[SF], g, sms, false).time;
-  const int64_t wide = estimate(kWide[SF], g, sms, false).time;
-  if (few.time <= one && few.time <= pair && few.time <= wide) {
-    if (g.M <= 16) return launch_few<GemmFp8FewConfig<16, OT, SF>>(p, few.split);
-    if (g.M <= 32) return launch_few<GemmFp8FewConfig<32, OT, SF>>(p, few.split);
-    return launch_few<GemmFp8FewConfig<64, OT, SF>>(p, few.split);
-  }
-  return g.vec != 0 ? launch_tiles<OT, SF, true>(p, one, pair, wide) : launch_tiles<OT, SF, false>(p, one, pair, wide);
+  int sms = 0;
+  fp4q_status st = current_sms(&sms);
+  if (st != FP4Q_OK) return st;
+  const Choice c = choose(SF, p.g, sms);
+  if (c.v == &kFew16) return launch_few<GemmFp8FewConfig<16, OT, SF>>(p, c.split);
+  if (c.v == &kFew32) return launch_few<GemmFp8FewConfig<32, OT, SF>>(p, c.split);
+  if (c.v == &kFew64) return launch_few<GemmFp8FewConfig<64, OT, SF>>(p, c.split);
+  return p.g.vec != 0 ? launch_tiles<OT, SF, true>(c.v, p) : launch_tiles<OT, SF, false>(c.v, p);
 }
 
 template <int OT>
@@ -183,6 +208,23 @@ fp4q_status dispatch_sf(int scale_format, const Problem& p) {
 }
 
 }  // namespace
+
+fp4q_status gemm_fp8_choice(int scale_format, int64_t M, int64_t N, int64_t K, int sms, int* tile_m, int* tile_n,
+                            int* split) {
+  if (sms == 0) {
+    fp4q_status st = current_sms(&sms);
+    if (st != FP4Q_OK) return st;
+  }
+  GemmFp8Args g = {};
+  g.M = M;
+  g.N = N;
+  g.kb = static_cast<int>((K + kFp8Block - 1) / kFp8Block);
+  const Choice c = choose(scale_format, g, sms);
+  *tile_m = c.v->tile_m;
+  *tile_n = c.v->tile_n;
+  *split = c.split;
+  return FP4Q_OK;
+}
 
 fp4q_status launch_gemm_fp8(int scale_format, int out_dtype, const void* a_codes, const void* a_scales,
                             const void* b_codes, const void* b_scales, int64_t M, int64_t N, int64_t K, void* d,

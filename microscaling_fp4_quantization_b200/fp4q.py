@@ -54,6 +54,7 @@ _SIGS = {
     "fp4q_gemm_fp8": (_int, [_int, _int, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]),
     "fp4q_device_status": (_int, []),
     "fp4q_selftest_wait_timeout": (_int, [_vp]),
+    "fp4q_selftest_gemm_fp8_choice": (_int, [_int, _i64, _i64, _i64, _int] + [ctypes.POINTER(_int)] * 3),
     "fp4q_status_string": (ctypes.c_char_p, [_int]),
     "fp4q_last_cuda_error": (ctypes.c_char_p, []),
     "fp4q_version": (_int, []),
@@ -241,6 +242,14 @@ def fp4q_device_status() -> int:
 def fp4q_selftest_wait_timeout(stream=None) -> None:
     """One warp whose bounded wait runs out: the next fp4q_device_status is FP4Q_ERR_TIMEOUT."""
     _check(_lib.fp4q_selftest_wait_timeout(_stream(stream)), "fp4q_selftest_wait_timeout")
+
+
+def fp4q_selftest_gemm_fp8_choice(scale_format: int, M: int, N: int, K: int, sm_count: int = 0) -> Tuple[int, int, int]:
+    """(rows, columns) of the tile of D that fp4q_gemm_fp8 takes for these sizes, and the CTAs K is split over."""
+    out = [_int() for _ in range(3)]
+    _check(_lib.fp4q_selftest_gemm_fp8_choice(scale_format, M, N, K, sm_count, *map(ctypes.byref, out)),
+           "fp4q_selftest_gemm_fp8_choice")
+    return tuple(v.value for v in out)
 
 
 def fp4q_status_string(status: int) -> str:
