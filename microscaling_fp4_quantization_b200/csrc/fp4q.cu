@@ -950,8 +950,10 @@ const char* fp4q_status_string(fp4q_status status) {
   switch (status) {
     case FP4Q_OK: return "ok";
     case FP4Q_ERR_ARG: return "invalid argument";
-    case FP4Q_ERR_SHAPE: return "invalid shape (a size outside the call's shape rules)";
-    case FP4Q_ERR_ALIGN: return "pointer not aligned (16 bytes for arrays, 4 for fp32 scales)";
+    case FP4Q_ERR_SHAPE:
+      return "invalid shape (K must be a multiple of max(group, hadamard_block), of 256 in fp4q_gemm, of 16 in the "
+             "8-bit calls; or a size or row distance outside the call's shape rules)";
+    case FP4Q_ERR_ALIGN: return "pointer not aligned (16 bytes for arrays, 4 for the tensor scale and fp32 scales)";
     case FP4Q_ERR_UNSUPPORTED: return "unsupported format / group / block / rule";
     case FP4Q_ERR_CUDA: return "CUDA error";
     case FP4Q_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
