@@ -287,7 +287,8 @@ fp4q_status fp4q_quantize_fp8(int scale_format, int dtype, int block_rows, const
  * x itself (with ldo = ldx).  eps: finite, >= 0.  K at most 32768; the rest as for fp4q_quantize_fp8.
  * The sum of squares is fp32, in a fixed order: the result of a row depends on that row, weight, eps and
  * K alone.  Rows whose sum of squares passes fp32's range give zeros, as 1 / sqrt(inf) does; a row of zeros
- * with eps = 0 gives NaN. */
+ * with eps = 0 gives NaN, and so does one whose squares all fall below it (magnitudes under 2^-75; under 2^-63
+ * squares lose bits, which eps = 0 shows too). */
 fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int64_t ldx, const void* residual,
                                  int64_t ldr, const void* weight, float eps, int64_t M, int64_t K,
                                  void* residual_out, int64_t ldo, void* codes_out, void* scales_out, void* stream);

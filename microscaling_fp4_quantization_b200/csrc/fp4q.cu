@@ -2,6 +2,7 @@
 // host-side validation, kernel selection and launch on the caller's stream.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -869,7 +870,7 @@ fp4q_status fp4q_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, int
   if (!valid_fp8_scale(scale_format) || (dtype != FP4Q_DTYPE_BF16 && dtype != FP4Q_DTYPE_FP16))
     return FP4Q_ERR_UNSUPPORTED;
   if ((residual != nullptr) != (residual_out != nullptr)) return FP4Q_ERR_ARG;
-  if (!(eps >= 0.0f) || eps > 3.0e38f) return FP4Q_ERR_ARG;   // negative, NaN or infinite
+  if (!(eps >= 0.0f) || std::isinf(eps)) return FP4Q_ERR_ARG;   // negative, NaN or infinite
   fp4q_status st = check_fp8_rows(M, K, ldx);
   if (st == FP4Q_OK && residual) st = check_fp8_rows(M, K, ldr);
   if (st == FP4Q_OK && residual) st = check_fp8_rows(M, K, ldo);
