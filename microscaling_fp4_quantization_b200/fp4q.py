@@ -330,9 +330,13 @@ def _fp8_init() -> None:
     _fp8_in_dtypes.update({torch.bfloat16: FP4Q_DTYPE_BF16, torch.float16: FP4Q_DTYPE_FP16})
     _fp8_out_dtypes.update(_fp8_in_dtypes)
     _fp8_out_dtypes[torch.float32] = FP4Q_DTYPE_F32
-    _fp8_scale_dtypes.update({FP4Q_FP8_SCALE_F32: torch.float32, FP4Q_FP8_SCALE_E8M0: torch.float8_e8m0fnu})
+    _fp8_scale_dtypes[FP4Q_FP8_SCALE_F32] = torch.float32
+    if hasattr(torch, "float8_e8m0fnu"):   # else only float32 scales are offered
+        _fp8_scale_dtypes[FP4Q_FP8_SCALE_E8M0] = torch.float8_e8m0fnu
     _e4m3 = torch.float8_e4m3fn
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # (not a public name)
+    if _raw_stream is None:
+        _raw_stream = lambda index: torch.cuda.current_stream(index).cuda_stream
     _current_device = torch.cuda.current_device
     _torch = torch
 
@@ -466,7 +470,7 @@ def gemm_fp8(a_codes, a_scales, b_codes, b_scales, out_dtype=None, out=None, str
     (M, K), N = shape, b_shape[0]
     kb = -(-K // 128)
     fmt = FP4Q_FP8_SCALE_F32 if s_dtype is _torch.float32 else FP4Q_FP8_SCALE_E8M0
-    if s_dtype is not _fp8_scale_dtypes[fmt]:
+    if s_dtype is not _fp8_scale_dtypes.get(fmt):
         raise ValueError("the scales must be float32 or float8_e8m0fnu")
     _fp8_array("a_codes", a_codes, shape, _e4m3, index)
     _fp8_array("b_codes", b_codes, (N, K), _e4m3, index)
