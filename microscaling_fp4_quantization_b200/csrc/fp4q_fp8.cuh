@@ -1,6 +1,9 @@
 // 8-bit (E4M3) quantization with a scale per 128 channels: the quantizer (a scale per row and
 // 128 channels, or per 128 x 128 tile) and the RMS norm, with the residual's addition, that ends
 // in it.  The rules of the scale and of the codes are in fp4q.h (fp4q_quantize_fp8).
+//
+// Times: us a launch, launches back to back in a graph on bf16 inputs that pass L2 in turn.  The tensor call shows
+// its host time where that is longer (6 to 9 us), and a little more where it is not (large norm 146, call 158).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,9 +64,9 @@ __device__ __forceinline__ uint32_t e4m3x4(f32x2 a, f32x2 b) {
 
 // The scale of a block whose largest magnitude has the fp32 bit pattern A (sign clear), and what
 // the elements are divided by: v = y / s.
-//   F32   s = max(RN(A / 448), 2^-126); the quotient is corrected once, so it is the correctly
-//         rounded one while s >= 2^-90 (below, the correction's remainder falls under fp32's range
-//         and v may be one ulp off);
+//   F32   s = max(RN(A / 448), 2^-126); the quotient is corrected once by its remainder (Markstein's step, as
+//         div_rn_markstein), so it is the correctly rounded one while s >= 2^-90 (below, the remainder
+//         falls under fp32's range and v may be one ulp off);
 //   E8M0  s = 2^e, byte e + 127, e = ceil(log2(A / 448)) >= -126, from A's bits: 448 = 1.75 * 2^8;
 //         the product with 2^-e is exact.
 // An infinity or a NaN in the block gives the scale NaN (byte 255), and so NaN codes.
@@ -139,9 +142,9 @@ struct Fp8QuantArgs {
 // One pass: eight lanes hold a block (16 channels each, two 16-byte loads and one 16-byte store),
 // its maximum takes three shuffles, and a warp's four blocks are neighbours in memory.  The floor
 // is the traffic, 3 bytes an element.  A CTA does 32 blocks and leaves: the next one's loads start
-// as soon as there is room, where the CTAs of a persistent grid load and store in step.  32768 x 14336
-// bf16: 198 us, 7.1 TB/s, against 251 us on a persistent grid of one wave and 228 us with two waves of
-// four blocks to a group of lanes.
+// as soon as there is room, where the CTAs of a persistent grid load and store in step.  32768 x 14336:
+// 204 us, 7.0 TB/s (E8M0 196); in one run of variants 198 us, 251 on a persistent grid of one wave and 228
+// with two waves of four blocks to a group of lanes.
 constexpr int kFp8QuantThreads = 256;
 
 template <int DT>
@@ -188,8 +191,8 @@ __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_rows_kernel(Fp8
 //
 // One CTA per tile, held in registers (64 elements a thread: four rows 32 apart), so that it is
 // read once; the maximum goes over a warp by shuffles and over the CTA's eight warps through
-// shared memory.  14336 x 4096 bf16: 27.2 us, 6.5 TB/s, bound by the traffic (with 512 threads a tile,
-// 27.7 to 34.6 us).
+// shared memory.  14336 x 4096: 28.4 us, 6.2 TB/s (E8M0 26.9), bound by the traffic; in one run of variants
+// 27.2 us, and 27.7 to 34.6 with 512 threads a tile.
 template <int DT, int SF>
 __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_tiles_kernel(Fp8QuantArgs a) {
   __shared__ uint32_t s_max[kFp8QuantThreads / 32];
@@ -239,9 +242,20 @@ __global__ void __launch_bounds__(kFp8QuantThreads) quantize_fp8_tiles_kernel(Fp
 //
 // A CTA takes whole rows, one after another, and holds a row in registers between its one read and
 // its one write: C chunks of 16 channels a thread.  C = 2 where there are many rows (smaller CTAs, more
-// of them on an SM in different phases: 16384 x 8192 bf16 takes 146 us, 6.4 TB/s, against 156 us with
-// C = 1 and 182 us with C = 4); C = 1 where a row has an SM to itself and its latency counts (1 x 4096:
-// 2.3 us against 3.0).  h, the square sum and y stay in fp32: y is rounded once, to its code, and the
+// of them on an SM in different phases), C = 1 where a row has an SM to itself and its latency counts.
+// C = 4 took 182 us at 16384 x 8192.  Measured, us with C = 1 / 2, by channels (down) and rows:
+//                1           148         149         333         600         1200        2400        16384
+//   with a residual
+//     4096   2.0 / 2.6   2.7 / 3.7   3.1 / 3.8   4.2 / 6.1   5.3 / 6.4   8.2 / 8.9  13.7 / 14.1   76 / 73
+//     5008   2.2 / 2.8   3.0 / 4.1   3.7 / 4.3   4.5 / 6.3   6.9 / 7.1  10.1 / 10.8 17.1 / 17.4  101 / 97
+//     8192   2.6 / 3.0   3.8 / 4.5   4.2 / 5.0   6.8 / 6.8   9.3 / 9.5  15.1 / 14.9 26.3 / 26.3  157 / 146
+//    14336   3.6 / 4.0   5.1 / 5.8   7.4 / 6.2  10.9 / 10.7 16.9 / 15.2 28.5 / 26.7 50.5 / 46.2  305 / 276
+//   without
+//     4096   1.9 / 2.4   2.1 / 2.6   2.5 / 2.8   3.4 / 3.5   3.9 / 5.1   6.3 / 5.8   9.4 / 9.7    52 / 47
+//     8192   2.2 / 2.6   2.8 / 3.4   3.1 / 3.7   5.5 / 5.2   7.3 / 7.3  11.9 / 10.6 20.0 / 18.4  116 / 100
+//    14336   2.7 / 3.0   3.7 / 4.3   5.5 / 4.7   8.6 / 8.3  13.2 / 11.7 22.6 / 19.6 40.9 / 33.4  247 / 195
+// The border at one row to an SM suits long rows; up to 5008 channels C = 1 stays ahead to some 2400 rows, by
+// 2 us at most.  h, the square sum and y stay in fp32: y is rounded once, to its code, and the
 // norm is of h as it was before it is rounded to be stored.  The square sum goes over a chunk, then over
 // groups of 32 chunks, then over the groups: one order for both values of C, so that a row's result does not
 // depend on the batch it is in.

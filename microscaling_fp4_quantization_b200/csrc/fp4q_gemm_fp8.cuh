@@ -14,6 +14,12 @@
 // D is rounded once, to its type.  All three have a TMA producer warp and an MMA warp; the codes travel
 // through a ring of 128-byte-swizzled stages of one K-block, and several accumulators in tensor memory
 // let MMAs run while what they left before is read.  Every wait is bounded.
+//
+// Times in this file are of two kinds.  Those of a kernel as it stands are launches of fp4q_gemm_fp8 back to back
+// in a graph, on operands that the quantizers made of activations and weights and that pass L2 in turn; boxes
+// differ by 5 to 10 %, most where the power cap holds the clock.  Those that compare variants (marked "variants")
+// are of single kernels on codes of random bytes, which draw less power, so that large products run faster:
+// they compare with one another alone.
 #pragma once
 
 #include <cuda.h>
@@ -187,10 +193,10 @@ __device__ __forceinline__ void store_row16(const GemmFp8Args& g, int64_t row, i
 // Sixteen columns of a warp's 32 rows (lane: row) where rows keep no such alignment: by way of shared
 // memory (`buf`, kUnalignedBytes of the warp's own), so that neighbouring lanes store neighbouring
 // columns.  With a lane to a row, every store of 2 bytes would touch a sector of its own.
-// Measured, bf16, a lane to a row and this way: 793 x 11180 x 6784 197 and 96 us (256 x 256 tiles), 175 and
-// 81 us (E8M0); N = 11181, stores of single elements, 197 and 107 us, 175 and 86 us; N = 11184, rows of 16-byte
-// alignment, 82 and 75 us.  UNROLL: 16 where 64 sums a thread leave the registers for it (104 -> 101 us with
-// 128 x 128 tiles), else 4.  All lanes take part.
+// Variants, bf16, a lane to a row and this way: 793 x 11180 x 6784 197 and 96 us (256 x 256 tiles), 175 and
+// 81 us (E8M0); N = 11181, stores of single elements, 197 and 107 us, 175 and 86 us; UNROLL 16, where 64 sums
+// a thread leave the registers for it, 104 -> 101 us with 128 x 128 tiles, else 4.  As it stands, N = 11180 / 11181 /
+// 11184 (rows of 16-byte alignment): 99 to 124 / 111 / 86 us, E8M0 91 to 124 / 91 / 83.  All lanes take part.
 constexpr int kUnalignedPitch = 17, kUnalignedBytes = 32 * kUnalignedPitch * 4;
 template <int OT, int UNROLL>
 __device__ __forceinline__ void store_unaligned16(const GemmFp8Args& g, int64_t row0, int64_t col, const f32x2* acc,
@@ -263,17 +269,18 @@ __device__ __forceinline__ void lds_pairs(uint32_t addr, f32x2& a, f32x2& b) {
 // columns: its multiplier is one number a block, sa[row][j] * sb[n / 128][j], and a block costs it
 // one fused multiply-add per element.  Persistent, round-robin over the tiles.  C = 2 pairs the CTAs
 // of a cluster on one tile (cta_group::2, M = 256): each loads its 128 rows of A and half of B's, and
-// the leader issues the MMAs of both; that halves what B costs L2 and shared memory (8192^3: 593 us
-// against 627 us with one CTA to a 128 x 256 tile, when it was taken up).
+// the leader issues the MMAs of both; that halves what B costs L2 and shared memory (variants at 8192^3:
+// 593 us against 627 us with one CTA to a 128 x 256 tile, when it was taken up).
 //
-// What bounds it, measured at 8192^3: the MMAs and copies alone take 440 us (at a clock the power cap
-// holds near 1.3 GHz), with the adding 522 us.  A block's turn through one of the two accumulators is MMAs
-// (600 cycles with their start), commit and wake-up (290), the adding warps' read (500 - 590, in steps of
-// 8 columns: 16, 32 or 64 at a time take 619, 755 and 598 us) and the arrival that frees it (300); more
-// accumulators of narrower tiles cost more in operand traffic than they hide (256 x 128: 613 us).
+// 8192^3 takes 549 to 589 us, 333 x 4104 x 5008 16.7 to 18.7.  What bounds it, variants at 8192^3: the MMAs
+// and copies alone take 440 us (at a clock the power cap holds near 1.3 GHz), with the adding 522 us.  A
+// block's turn through one of the two accumulators is MMAs (600 cycles with their start), commit and wake-up
+// (290), the adding warps' read (500 - 590, in steps of 8 columns: 16, 32 or 64 at a time take 619, 755 and
+// 598 us) and the arrival that frees it (300); more accumulators of narrower tiles cost more in operand
+// traffic than they hide (256 x 128: 613 us).
 
 // Tile t's row and column of tiles: down kTileGroup rows, then the next column, so that the tiles worked on
-// at one time (74 pairs: 16 rows by 4.6 columns) share their rows of A and of B in L2.  8192^3 takes
+// at one time (74 pairs: 16 rows by 4.6 columns) share their rows of A and of B in L2.  Variants at 8192^3:
 // 523 us with fp32 scales and 397 us with E8M0, against 555 and 440 us down all 32 rows; groups of 8 and
 // 32 rows lie between, and where A's rows are few there is no difference.
 constexpr int kTileGroup = 16;
@@ -287,7 +294,7 @@ __device__ __forceinline__ void gemm_fp8_tile(const GemmFp8Args& g, int t, int& 
 constexpr int kMmaTries = 64;   // times an MMA warp asks for its barriers before it suspends
 
 // ALIGNED: D's rows keep a 16-byte alignment.  A parameter: with both kinds of stores in one
-// kernel it took 5 % longer at 8192^3 (525 -> 553 us).
+// kernel it took 5 % longer at 8192^3 (variants: 525 -> 553 us).
 template <int CTAS, int BN_, int OT, int SF, bool ALIGNED>
 struct GemmFp8Config {
   static constexpr int kCtas = CTAS;
@@ -662,8 +669,9 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 // the MMAs: four warps, one per lane quarter, load four blocks' bytes of a row as one word and store it
 // (row r of the tile: lane r mod 32 of every quarter, column r / 32, byte j mod 4).
 //
-// Measured: 8192^3 in 397 us, 2.77 PFLOP/s, where adding in registers takes 570 us; 4096 x 8192 x 8192
-// keeps the tensor pipe 85 to 88 % busy (57 % when added in registers).  What bounds it is the power cap, and
+// Measured: 8192^3 in 450 to 473 us, 2.4 PFLOP/s, where adding in registers takes 549 to 589 (variants: 397 and
+// 523 us); 4096 x 14336 x 4096 in 201 to 215 us.  4096 x 8192 x 8192 keeps the tensor pipe 85 % busy (58 % when
+// added in registers).  What bounds it is the power cap, and
 // below that the MMAs.
 template <int OT, bool ALIGNED>
 struct GemmFp8MxConfig {
@@ -882,11 +890,12 @@ __global__ void __launch_bounds__(Cfg::kThreads, 1)
 // split over a cluster.  A CTA's sums then go to the CTA of the cluster that owns their token (pushed
 // into its shared memory), which adds them in the order of their ranks: no atomics, no workspace.
 //
-// Measured: 1 x 14336 x 4096 in 12.7 us, of which B's 58.7 MB stream in 8.3 us (7.1 TB/s); the rest is the
-// first load (1.7 us), the sums and stores (0.6 us) and the gap to the next launch.  16 x 4096 x 14336 with
-// K over 1 / 2 / 3 / 4 CTAs: 29.4 / 17.1 / 14.1 / 13.7 us.  With two smaller CTAs to an SM the early start
-// of the next launch put two CTAs of one grid on an SM beside idle ones (64 x 14336 x 4096: 26.6 us
-// against 14.9).
+// Measured, with weights that are not in L2 (and, in brackets, ones that are): 1 x 14336 x 4096 12.4 us (10.6),
+// 16 x 4096 x 14336 13.1 (10.6), 16 x 8192 x 8192 13.9 (11.3), 64 x 14336 x 4096 14.5 (13.3), 16 x 4096 x 4096 6.9
+// (5.7).  Of the first, B's 58.7 MB stream in 8.3 us (7.1 TB/s); the rest is the first load (1.7 us), the sums and
+// stores (0.6 us) and the gap to the next launch.  Variants: 16 x 4096 x 14336 with K over 1 / 2 / 3 / 4 CTAs
+// 29.4 / 17.1 / 14.1 / 13.7 us; with two smaller CTAs to an SM the early start of the next launch put two CTAs
+// of one grid on an SM beside idle ones (64 x 14336 x 4096: 26.6 us against 14.9).
 template <int BT_, int OT, int SF>
 struct GemmFp8FewConfig {
   static constexpr int kBT = BT_, kBK = kFp8Block;

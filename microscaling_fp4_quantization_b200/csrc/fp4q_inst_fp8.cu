@@ -70,7 +70,7 @@ fp4q_status launch_add_rmsnorm_fp8(int scale_format, int dtype, const void* x, i
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  const int per_thread = M <= sms && chunks <= kFp8NormThreads ? 1 : 2;   // see the kernel
+  const int per_thread = M <= sms && chunks <= kFp8NormThreads ? 1 : 2;   // both are timed beside the kernel
   auto launch = [&]<int DT, int SF, int C, bool RES>() -> fp4q_status {
     auto kernel = add_rmsnorm_fp8_kernel<DT, SF, C, RES>;
     const int threads = ((chunks + C - 1) / C + 31) / 32 * 32;

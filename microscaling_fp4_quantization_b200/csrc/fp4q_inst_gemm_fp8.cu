@@ -116,9 +116,9 @@ fp4q_status launch_few(Problem p, int split) {
 // SMs, and one for each block of K that a round works off (units of 10 ns).  The costs are fitted to
 // measurements of all four kernels at M = 1 ... 4096 and nine pairs of N and K (1024 x 4096 to
 // 8192 x 8192, 600 x 784): over those the choice takes 0.7 % longer than the fastest of the four on
-// average (1.7 % with one cost per block alone).  Examples, in us as few / 128 x 128 / 256 x 128 / wide:
-// 96 x 8192 x 8192 25.6 / 24.6 / 23.7 / 34.5; 333 x 4104 x 5008 31.3 / 20.4 / 17.8 / 24.4; 256 x 4096 x
-// 4096 13.5 / 13.9 / 13.6 / 20.4; 1024 x 4096 x 4096 E8M0 49.4 / 27.3 / 27.9 / 22.7.
+// average (1.7 % with one cost per block alone).  Examples, of single kernels on random codes, in us as
+// few / 128 x 128 / 256 x 128 / wide: 96 x 8192 x 8192 25.6 / 24.6 / 23.7 / 34.5; 333 x 4104 x 5008 31.3 / 20.4 /
+// 17.8 / 24.4; 256 x 4096 x 4096 13.5 / 13.9 / 13.6 / 20.4; 1024 x 4096 x 4096 E8M0 49.4 / 27.3 / 27.9 / 22.7.
 struct Variant {
   int tile_m, tile_n;   // of D
   int ctas;             // per tile
