@@ -104,9 +104,15 @@ def _allocating_on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     import torch
+    _check_stream(stream, device.index)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     return torch.cuda.stream(stream)
+
+
+def _check_stream(stream, index: int) -> None:
+    if not isinstance(stream, int) and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on CUDA device {index}")
 
 
 class Plan:
@@ -367,14 +373,8 @@ def _fp8_empty(shape, dtype, index, stream):
     """An output of a call on `stream`."""
     if stream is None:
         return _torch.empty(shape, dtype=dtype, device=index)
-    _fp8_check_stream(stream, index)
-    with _allocating_on(stream, index):
+    with _allocating_on(stream, _torch.device("cuda", index)):
         return _torch.empty(shape, dtype=dtype, device=index)
-
-
-def _fp8_check_stream(stream, index) -> None:
-    if not isinstance(stream, int) and stream.device.index != index:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on CUDA device {index}")
 
 
 def _fp8_call(name: str, index: int, stream, *args) -> None:
@@ -382,7 +382,7 @@ def _fp8_call(name: str, index: int, stream, *args) -> None:
     if stream is None:
         stream = _raw_stream(index)
     elif not isinstance(stream, int):
-        _fp8_check_stream(stream, index)
+        _check_stream(stream, index)
         stream = stream.cuda_stream
     if _current_device() == index:
         status = getattr(_lib, name)(*args, stream)

@@ -155,9 +155,11 @@ def test_error_pass_waits_for_the_given_stream(F, fmt, kind):
 def test_a_stream_of_another_device_is_refused(F, operands):
     class Elsewhere:
         device, cuda_stream = torch.device("cuda", 1), 0
-    for name in ("quantize", "norm", "product"):
+    for name in NAMES:
         with pytest.raises(ValueError):
             calls(F, operands)[name](Elsewhere())
+    with pytest.raises(ValueError):
+        F.quant_error(operands[-1], operands[0], stream=Elsewhere())
 
 
 def test_a_captured_call_on_a_given_stream(F, operands):
