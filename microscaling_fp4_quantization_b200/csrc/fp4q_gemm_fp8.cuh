@@ -16,7 +16,7 @@
 // let MMAs run while what they left before is read.  Every wait is bounded.
 //
 // Times in this file are of two kinds.  Those of a kernel as it stands are launches of fp4q_gemm_fp8 back to back
-// in a graph, on operands that the quantizers made of activations and weights and that pass L2 in turn; boxes
+// in a graph, on operands that the quantizers made of activations and weights and that pass L2 in turn; GPUs
 // differ by 5 to 10 %, most where the power cap holds the clock.  Those that compare variants (marked "variants")
 // are of single kernels on codes of random bytes, which draw less power, so that large products run faster:
 // they compare with one another alone.
